@@ -338,6 +338,97 @@ mk_status mk_matvec_engine(int32_t engine, const void* W, int32_t rows, int32_t 
                            int32_t nb, float* Y, int32_t n_sm, int32_t wait_limit_ms, void* stream);
 mk_status mk_matvec_engine_status(void* stream);
 
+/* ---- 4-bit KV cache ----
+ *
+ * No counterpart in the pages: stages of a decoder layer for callers that run the
+ * layers themselves (like the greedy head and the matvec above) or that park a
+ * handle's sequences.  The handle's own cache holds 16-bit K/V (mk_config.kv_dtype);
+ * this one holds 4-bit codes at 0.3125 of those bytes: 5 bytes per 8 values.
+ *
+ * A row (K or V of one position and kv head, head_dim values) is quantised in groups
+ * of 32 neighbouring values.  Per group, z = min rounded down to fp16, s = the
+ * smallest fp16 with z + 15 s >= max, codes = (x - z) / s rounded to the nearest
+ * integer, ties to even; the cache then stands for z + s * code, at most s / 2 from
+ * x.  A group that holds a NaN, an infinity or a magnitude above 32768 stands for
+ * NaN as a whole.
+ *
+ * Memory is the caller's, as with the weights: a pool of pages of MK_KV4_PAGE
+ * positions, and per batch a table of each sequence's pages.  Sequence lengths live
+ * on the device, so a captured graph can be replayed while they grow; the host gives
+ * their bounds.  A batch with numbers outside these bounds (cu not ascending from 0 to
+ * at most n_rows, a span above max_new, a length below 0 or above max_len) or a page
+ * id outside the pool is recorded in the cache's status word; the sequence or page it
+ * concerns is neither written nor read.  Calls that overlap on the GPU must not
+ * write the same positions, nor read what another writes. */
+#define MK_KV4_PAGE 64
+
+typedef struct {
+  void* pool;          /* device [n_layers][n_pages][n_kv_heads][mk_kv4_page_bytes], 16-byte aligned */
+  uint32_t* status;    /* device word, zeroed by the caller: bits of what went wrong so far
+                          (1 batch numbers, 2 page id, 4 a bounded wait ran out) */
+  int32_t n_layers, n_pages, n_kv_heads;
+  int32_t head_dim;    /* 64 or 128 */
+} mk_kv4_cache;
+
+typedef struct {
+  const int32_t* block_table;  /* device [n_seqs][max_pages]: page of positions 64 j .. 64 j + 63 */
+  const int32_t* cu;           /* device [n_seqs + 1]: rows cu[i] .. cu[i + 1] - 1 belong to sequence i */
+  const int32_t* kv_lens;      /* device [n_seqs]: length in the cache, these rows included */
+  int32_t n_seqs, max_pages;
+  int32_t n_rows;              /* rows of the tensors; those from cu[n_seqs] on are left alone */
+  int32_t max_new;             /* bound of cu[i + 1] - cu[i] */
+  int32_t max_len;             /* bound of kv_lens, at most 64 * max_pages */
+} mk_kv4_batch;
+
+/* Rows in memory: bf16 (0), fp16 (1) or fp32 (2) values [row][head][head_dim], the
+ * last dimension contiguous, strides in elements; base and strides 16-byte aligned. */
+typedef struct {
+  void* p;
+  int64_t row_stride, head_stride;
+} mk_kv4_rows;
+
+/* Bytes of one page of one kv head; 0 for an unsupported head_dim. */
+int64_t mk_kv4_page_bytes(int32_t head_dim);
+
+/* Quantise the batch's K and V rows into a layer of the cache: row j of sequence i
+ * becomes position kv_lens[i] - (cu[i+1] - cu[i]) + j.  Asynchronous. */
+mk_status mk_kv4_append(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
+                        const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream);
+
+/* Read the same rows back: the values the cache stands for, rounded to dtype.
+ * Asynchronous. */
+mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
+                      const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream);
+
+/* Causal attention of the batch's query rows over the cache:
+ *   out[r][h] = sum_p softmax_p(scale * q[r][h] . K[p][h / rep]) V[p][h / rep],
+ * p over positions 0 .. kv_lens[i] - (cu[i+1] - cu[i]) + j of row j of sequence i,
+ * rep = n_heads / n_kv_heads in {1, 2, 4, 8}.  A row that sees no position (its
+ * sequence is shorter than its span) is zero.  Scores, softmax and sums are fp32.
+ * One new token per sequence or a few, whole prompts, and any mix run here; work is
+ * split along the positions when there are few rows, which takes `workspace` (device,
+ * 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when that is 0): concurrent
+ * calls need one each, and nothing is kept in it.  q and out have type dtype.
+ * Asynchronous. */
+mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
+                           const mk_kv4_rows* q, const mk_kv4_rows* out, int32_t n_heads, int32_t dtype,
+                           float scale, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of mk_kv4_attention for these bounds on the current device (host only). */
+mk_status mk_kv4_attention_workspace(const mk_kv4_cache* cache, const mk_kv4_batch* batch, int32_t n_heads,
+                                     int32_t dtype, int64_t* bytes);
+
+/* Park positions start .. start + n - 1 of a handle's slot: quantise its K/V of every
+ * layer into layers 0 .. n_layers - 1 of `cache`, at the same positions of the
+ * sequence whose pages block_table_row (device int32[max_pages]) names.  Resume
+ * writes the cached values back into a slot, rounded to the handle's K/V type, so
+ * that decoding continues at position start + n.  The cache's n_layers, n_kv_heads
+ * and head_dim must be the handle's.  Asynchronous; ordered like the handle's steps. */
+mk_status mk_kv4_park(mk_handle h, int32_t slot, int32_t start, int32_t n, const mk_kv4_cache* cache,
+                      const int32_t* block_table_row, int32_t max_pages, void* stream);
+mk_status mk_kv4_resume(mk_handle h, int32_t slot, int32_t start, int32_t n, const mk_kv4_cache* cache,
+                        const int32_t* block_table_row, int32_t max_pages, void* stream);
+
 /* Library version string (static storage). */
 const char* mk_version(void);
 

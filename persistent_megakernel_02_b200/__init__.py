@@ -18,7 +18,7 @@ import os
 from .build import LIB
 
 __all__ = ["Megakernel", "MkError", "plan_check", "version", "lib", "STATUS",
-           "greedy_head_noalloc", "rope_inv_freq"]
+           "greedy_head_noalloc", "rope_inv_freq", "Kv4Cache", "Kv4Batch"]
 
 STATUS = {
     0: "MK_OK",
@@ -84,6 +84,30 @@ class MkPlanReport(ctypes.Structure):
     ]
 
 
+class MkKv4CacheStruct(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p), ("status", ctypes.c_void_p), ("n_layers", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+    ]
+
+
+class MkKv4Batch(ctypes.Structure):
+    _fields_ = [
+        ("block_table", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+        ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int32),
+    ]
+
+
+class MkKv4Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+_KV4_ROWS = [ctypes.POINTER(MkKv4CacheStruct), ctypes.c_int32, ctypes.POINTER(MkKv4Batch),
+             ctypes.POINTER(MkKv4Rows), ctypes.POINTER(MkKv4Rows)]
+_KV4_SLOT = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(MkKv4CacheStruct),
+             ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+
 # exported entry points and their signatures (kept in step with include/mk.h)
 _SIGS = {
     "mk_create": (ctypes.c_int, [ctypes.POINTER(MkConfig), ctypes.POINTER(MkWeights),
@@ -121,6 +145,15 @@ _SIGS = {
                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_void_p]),
     "mk_matvec_engine_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "mk_kv4_page_bytes": (ctypes.c_int64, [ctypes.c_int32]),
+    "mk_kv4_append": (ctypes.c_int, _KV4_ROWS + [ctypes.c_int32, ctypes.c_void_p]),
+    "mk_kv4_read": (ctypes.c_int, _KV4_ROWS + [ctypes.c_int32, ctypes.c_void_p]),
+    "mk_kv4_attention": (ctypes.c_int, _KV4_ROWS + [ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p,
+                                                    ctypes.c_int64, ctypes.c_void_p]),
+    "mk_kv4_attention_workspace": (ctypes.c_int, [ctypes.POINTER(MkKv4CacheStruct), ctypes.POINTER(MkKv4Batch),
+                                                  ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]),
+    "mk_kv4_park": (ctypes.c_int, _KV4_SLOT),
+    "mk_kv4_resume": (ctypes.c_int, _KV4_SLOT),
     "mk_version": (ctypes.c_char_p, []),
 }
 
@@ -297,6 +330,7 @@ class Megakernel:
                         dyn_percent=dyn_percent, prefill_tokenwise=prefill_tokenwise,
                         region_cut=region_cut, tensor_core_units=tensor_core_units)
         self._cfg_struct = config_struct(cfg)
+        self._device = device
         h = ctypes.c_void_p()
         _check(lib().mk_create(ctypes.byref(self._cfg_struct), ctypes.byref(w), ctypes.byref(opt),
                                ctypes.byref(h)), "mk_create")
@@ -355,6 +389,30 @@ class Megakernel:
                "mk_prefill")
         return out.value if want_id else None
 
+    def _move_slot(self, fn, what, slot, n, cache, seq, start, block_table, stream):
+        table = cache.block_table if block_table is None else block_table
+        import torch
+
+        if table is None or table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous() or \
+                table.device != cache.device or not 0 <= seq < table.shape[0]:
+            raise MkError(1, f"{what}: block_table must be a contiguous int32 [n_seqs, max_pages] tensor on the "
+                             "cache's device with a row for the sequence")
+        if cache.device.index != self._device:
+            raise MkError(1, f"{what}: the cache is not on the handle's device ({self._device})")
+        _check(fn(self._h, slot, start, n, cache._ref, table.data_ptr() + 4 * int(table.shape[1]) * seq,
+                  int(table.shape[1]), _stream_handle(stream)), what)
+
+    def park(self, slot, n, cache, seq, start=0, block_table=None, stream=None):
+        """Quantise positions start .. start + n - 1 of slot ``slot``, every layer, into
+        sequence ``seq`` of a :class:`Kv4Cache` (a row of its block table); the slot can then
+        take another sequence.  Asynchronous, ordered like the handle's steps."""
+        self._move_slot(lib().mk_kv4_park, "mk_kv4_park", slot, n, cache, seq, start, block_table, stream)
+
+    def resume(self, slot, n, cache, seq, start=0, block_table=None, stream=None):
+        """Write the parked positions back into slot ``slot`` (any slot), rounded to the
+        handle's K/V type; decoding continues at position start + n."""
+        self._move_slot(lib().mk_kv4_resume, "mk_kv4_resume", slot, n, cache, seq, start, block_table, stream)
+
     def profile_records(self):
         """Per-instruction profile records: int64 array [n_sm, stride, 32] (see mk_profile_read)."""
         import numpy as np
@@ -391,3 +449,6 @@ class Megakernel:
             self.close()
         except Exception:
             pass
+
+
+from .kv4 import Kv4Batch, Kv4Cache  # noqa: E402  (the module uses the names above)

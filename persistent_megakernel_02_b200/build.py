@@ -27,9 +27,11 @@ UNITS = [
     ("mk_noalloc", "mk_noalloc.cu", []),
     ("mk_engines", "mk_engines.cu", []),
     ("mk_prefill", "mk_prefill.cu", []),
+    ("mk_kv4", "mk_kv4.cu", []),
+    ("mk_kv4_attn", "mk_kv4_attn.cu", []),
 ] + [(f"mk_inst_s{s}_n{n}", "mk_inst.cu", [f"-DMK_SPEC={s}", f"-DMK_NBT={n}"])
      for s in (0, 1, 2) for n in (8, 4, 2, 1)]
-DEPS = ["mk_kernel.cuh", "mk_device.cuh", "mk_matvec.cuh", "mk_plan.h", "mk_tc.cuh"]
+DEPS = ["mk_kernel.cuh", "mk_device.cuh", "mk_matvec.cuh", "mk_plan.h", "mk_tc.cuh", "mk_kv4.cuh", "mk_kv4.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC"]
 

@@ -1,0 +1,21 @@
+// mk_kv4.h -- host-side pieces of the 4-bit KV cache shared by its translation units
+// and by the handle (mk_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/mk.h"
+
+namespace mk {
+
+mk_status kv4_check_cache(const mk_kv4_cache* c);
+mk_status kv4_check(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, int32_t dtype);
+// `written`: the rows are an output, so they must not overlap
+mk_status kv4_check_rows(const mk_kv4_rows* r, int32_t dtype, int64_t rows, int32_t heads, int32_t d, bool written);
+
+// Quantise (write) or read back positions start .. start + n - 1 of a slot of a handle's
+// cache [layer][physical page][kv head][K, V][PL][d], all layers; arguments checked by the caller.
+mk_status kv4_slot(bool write, const mk_kv4_cache* c, void* kv, const int* slot_table, int n_phys_pages, int PL,
+                   bool fp16, const int32_t* table_row, int start, int n, cudaStream_t s);
+
+}  // namespace mk
