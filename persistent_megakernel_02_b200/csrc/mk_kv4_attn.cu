@@ -1,7 +1,30 @@
-// mk_kv4_attn.cu -- causal attention over the 4-bit KV cache.
+// mk_kv4_attn.cu -- causal attention over the 4-bit KV cache for few query rows: single
+// new tokens, a few at a time, and every 32-bit call.
+//
+// Mathematics.  With K = z + s c per group g of 32 values, a score is
+//   q . K = sum_g s_g (q_g . c_g) + sum_g z_g (sum of q_g),
+// so the codes enter the matrix instructions as they are: a 4-bit code in the low bits
+// of an fp16 word is the subnormal c 2^-24 (or 16 c 2^-24 from the next nibble, with
+// the query divided by 16 instead), exact in the products and sums of mma.m16n8k16.
+// One AND turns 32 bits of codes into two operand values, and only the sums over 32
+// values are multiplied by a scale.  The second sum is one more mma over the groups.
+// Values the same way: O = sum_p w_p V_p = sum_g c (w s)_g + z_g w, the weights of a
+// position times its scale are the operand, and one mma holds the z part of all groups.
+// The softmax runs in one pass with a running maximum and sum per row; the operand w s
+// is kept in fp16's range by the running reference, which also counts the power of two
+// of the largest scale met so far.
+//
+// Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
+// A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
+// a ring of bulk copies of its own, so no barrier is met until the warps' states are
+// merged.  Splits along the positions, where rows are few, are joined by a second
+// small kernel.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "mk_kv4.cuh"
 #include "mk_kv4.h"
@@ -9,111 +32,616 @@
 namespace mk {
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kThreadsA = 32 * kWarps;
+constexpr int kStageBytes = 5120;
+constexpr int kStages = 3;  // ring depth per warp
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
 struct AttnArgs {
   mk_kv4_cache c;
   mk_kv4_batch b;
   const char* q;
   char* out;
   long long q_row, q_head, o_row, o_head;  // strides in bytes
-  int layer, n_heads, rep;
-  float scale;
+  int layer, rep;
+  float scale_log2;  // scale * log2(e)
+  int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page)
+  int n_rt;                // row tiles
+  float* part;             // [seq][kv head][row tile][split][8 NT][D + 2]
 };
 
-__device__ __forceinline__ int seq_of_row(const mk_kv4_batch& b, int row) {
-  int lo = 0, hi = b.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.cu[mid] <= row) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {  // a NaN loses
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// a pair of halves with each one cleared that is infinite or NaN
+__device__ __forceinline__ uint32_t finite2(uint32_t a) {
+  if ((a & 0x7C00u) == 0x7C00u) a &= 0xFFFF0000u;
+  if ((a & 0x7C000000u) == 0x7C000000u) a &= 0xFFFFu;
+  return a;
+}
+// two fp16 parts of a pair of floats: x ~= hi + lo with 22 bits
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_h(x, y);
+  lo = pack_h(x - h_lo(hi), y - h_hi(hi));
 }
 
-// The plain form: a warp per query row and head, 32 positions at a time (a lane scores
-// one position), softmax with a running maximum and sum, a lane per D / 32 output values.
-template <int D, class T>
-__global__ void __launch_bounds__(128) attn_simple(AttnArgs a) {
+// Waits for a phase with a limit; on expiry the cache's status word says so.
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_hint(bar, parity, 1000)) {
+    if (globaltimer_ns() - t0 > kWaitNs) {
+      atomicOr(status, KV4_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// One CTA: the rows of a row tile (8 NT rows: query tokens x the rep heads of one kv
+// head) over one split of the positions, its stages dealt to the warps in turn.
+// Registers per lane (gid = lane / 4, tig = lane % 4), NT row tiles of 8:
+//   scores   row gid, positions 2 tig, 2 tig + 1 of each 8
+//   outputs  value 32 g + 4 gid + 2 j + {0, 1} of rows 2 tig, 2 tig + 1
+// 32-bit calls split queries and weights into two fp16 parts: the queries' low parts
+// are rows 8..15 of the same mma, the weights' take a second one.
+template <int D, class T, int NT>
+__global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   using L = Kv4<D>;
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x, hq = blockIdx.y * 4 + warp;
-  __shared__ float qs[4][D];
-  if (hq >= a.n_heads) return;
-  const int si = seq_of_row(a.b, row);
-  const Kv4Seq s = kv4_seq(a.b, si);
-  if (!s.ok) {
-    if (lane == 0) atomicOr(a.c.status, KV4_BAD_BATCH);
+  constexpr int G = L::G;
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int MT = kF32 ? NT : (NT + 1) / 2;          // 16-row operands of the queries
+  constexpr int kTilesPerStage = kStageBytes / L::kBytes;
+  constexpr int kStagePos = kTilesPerStage * kKv4Tile;  // positions of a stage
+  constexpr int kStagesPerPage = MK_KV4_PAGE / kStagePos;
+  constexpr int SUB = NT >= 4 ? 2 : kTilesPerStage;     // tiles per softmax step
+  constexpr int kRows = 8 * NT;
+
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ int slot_bad[kWarps][kStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  uint8_t* ring = smem + warp * (kStages * kStageBytes);
+
+  int idx = blockIdx.x;
+  const int split = idx % a.n_split;
+  idx /= a.n_split;
+  const int rt = a.n_rt - 1 - idx % a.n_rt;  // the tiles that see most come first
+  idx /= a.n_rt;
+  const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
+  const Kv4Seq seq = kv4_seq(a.b, si);
+  if (!seq.ok) {
+    if (threadIdx.x == 0) atomicOr(a.c.status, KV4_BAD_BATCH);
     return;
   }
-  if (row < s.row0 || row >= s.row0 + s.n) return;
-  const int head = hq / a.rep, see = s.len - s.n + (row - s.row0) + 1;  // positions seen
+  const int n_rows = seq.n * a.rep, row0 = rt * kRows;
+  if (row0 >= n_rows) return;
+  const int start = seq.len - seq.n;  // position of the first query token (may be negative)
+  const int last_row = min(n_rows, row0 + kRows) - 1;
+  const int see_all = start + row0 / a.rep + 1;                // positions every row of the tile sees
+  const int see_any = max(0, start + last_row / a.rep + 1);    // positions some row sees
+  const int p0 = split * a.split_len, p1 = min(see_any, p0 + a.split_len);
+  if (p0 >= p1 && split > 0) return;  // the merge takes only the splits that hold something
   const int32_t* table = a.b.block_table + (size_t)si * a.b.max_pages;
-  if (lane < D / 8) {
-    float x[8];
-    load8<T>(a.q + row * a.q_row + hq * a.q_head + lane * 8 * sizeof(T), x);
-    for (int i = 0; i < 8; ++i) qs[warp][lane * 8 + i] = x[i];
+
+  // ---- ring of bulk copies: this warp's stage i is stage s0 + warp + kWarps i ----
+  const int s0 = p0 / kStagePos, n_stages = p0 < p1 ? (p1 - 1) / kStagePos - s0 + 1 : 0;
+  const int mine = n_stages > warp ? (n_stages - warp - 1) / kWarps + 1 : 0;
+  int page_id = 0;  // lane i: page of this warp's stage (32 k + i)
+  auto issue = [&](int i) {  // every lane calls
+    if ((i & 31) == 0) {
+      const int j = i + lane;
+      page_id = j < mine ? table[(s0 + warp + kWarps * j) / kStagesPerPage] : 0;
+    }
+    const int page = __shfl_sync(0xFFFFFFFFu, page_id, i & 31);
+    if (lane == 0) {
+      const int s = s0 + warp + kWarps * i, slot = i % kStages;
+      const bool bad = (unsigned)page >= (unsigned)a.c.n_pages;
+      slot_bad[warp][slot] = bad;
+      if (bad) {
+        atomicOr(a.c.status, KV4_BAD_PAGE);
+        mbar_arrive(&full[warp][slot]);
+      } else {
+        const int tiles = min(kTilesPerStage, (p1 - s * kStagePos + kKv4Tile - 1) / kKv4Tile);
+        const size_t tile = (((size_t)a.layer * a.c.n_pages + page) * a.c.n_kv_heads + head) * kKv4Tiles +
+                            (s % kStagesPerPage) * kTilesPerStage;
+        mbar_arrive_expect_tx(&full[warp][slot], tiles * L::kBytes);
+        bulk_g2s_plain(ring + slot * kStageBytes, static_cast<const uint8_t*>(a.c.pool) + tile * L::kBytes,
+                       tiles * L::kBytes, &full[warp][slot]);
+      }
+    }
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
+    fence_barrier_init();
   }
   __syncwarp();
-  float m = -INFINITY, l = 0.f, o[E];
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int p0 = 0; p0 < see; p0 += 32) {
-    const int p = p0 + lane;
-    float sc = -INFINITY;
-    const uint8_t* tile = p < see ? kv4_tile<D>(a.c, table, a.layer, head, p / kKv4Tile) : nullptr;
-    if (p < see && !tile) atomicOr(a.c.status, KV4_BAD_PAGE);
-    const int r = p % kKv4Tile;
-    if (tile) {
-      float acc = 0.f;
-      for (int g = 0; g < L::G; ++g) {
-        float dot = 0.f, sum = 0.f;
-        for (int w = 4 * g; w < 4 * g + 4; ++w) {
-          const uint32_t codes = *reinterpret_cast<const uint32_t*>(tile + L::k_word(r, w));
-          for (int i = 0; i < 8; ++i) {
-            const float q = qs[warp][8 * w + i];
-            dot = fmaf(q, (float)((codes >> (4 * i)) & 15u), dot);
-            sum += q;
+  for (int i = 0; i < kStages && i < mine; ++i) issue(i);
+
+  // ---- queries: operand order of the codes, scaled by a power of two per row ----
+  uint32_t qa[MT][G][2][4];  // [16 rows][group][k16 step][a0..a3]
+  uint32_t qz[MT][4];        // sums over the groups, for the minima
+  float kscale[NT];          // score = kscale * accumulated
+  int lim[NT];               // positions the row sees
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 4; ++h) qz[m][h] = 0u;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + 8 * t + gid;
+    const bool live = r < n_rows;
+    float x[G][8];
+    float mx = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (live) {
+        load8<T>(a.q + (seq.row0 + r / a.rep) * a.q_row + (head * a.rep + r % a.rep) * a.q_head +
+                     (32 * g + 8 * tig) * (int)sizeof(T),
+                 x[g]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[g][i]));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    // power of two that brings the largest to 2^12 .. 2^13 (rows of zeros and rows
+    // with an infinity keep theirs)
+    const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + max(e, -126)) << 23);
+    kscale[t] = a.scale_log2 * 16777216.f / up;
+    lim[t] = live ? start + r / a.rep + 1 : 0;
+    float sums[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[g][i] *= up;
+        sum += x[g][i];
+      }
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      sums[g] = sum * 0.015625f;  // 2^-6: at most 2^12
+      // nibble i of a word is value 8 w + i; steps pair (0, 4), (1, 5) and (2, 6), (3, 7)
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint32_t h0, l0, h1, l1;
+        split2(x[g][2 * st], x[g][2 * st + 4], h0, l0);
+        split2(x[g][2 * st + 1] * 0.0625f, x[g][2 * st + 5] * 0.0625f, h1, l1);
+        if constexpr (kF32) {
+          qa[t][g][st][0] = h0;
+          qa[t][g][st][1] = l0;
+          qa[t][g][st][2] = h1;
+          qa[t][g][st][3] = l1;
+        } else {
+          qa[t / 2][g][st][t & 1] = h0;
+          qa[t / 2][g][st][2 + (t & 1)] = h1;
+          if constexpr (NT == 1) qa[0][g][st][1] = qa[0][g][st][3] = 0u;
+        }
+      }
+    }
+    // k index of the minima's mma: groups 2 tig, 2 tig + 1 (high parts), + 8 (low parts)
+    float s_lo = 0.f, s_hi = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; g += 2)
+      if (tig == g / 2) { s_lo = sums[g]; s_hi = sums[g + 1]; }
+    uint32_t zh, zl;
+    split2(s_lo, s_hi, zh, zl);
+    if constexpr (kF32) {
+      qz[t][0] = zh;
+      qz[t][2] = zl;
+    } else {
+      qz[t / 2][t & 1] = zh;
+      qz[t / 2][2 + (t & 1)] = zl;
+    }
+  }
+
+  float o[NT][G][2][4], oz[NT][4], m[NT], l[NT], ref[NT];
+  int lift = 14;  // weights are scaled by 2^lift: 14, or less where scales are large
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = ref[t] = -INFINITY;
+    l[t] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) oz[t][i] = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][g][j][i] = 0.f;
+  }
+
+  // SUB tiles at `tiles`, the first at position `pos`
+  auto step = [&](const uint8_t* tiles, int pos, auto masked_tag) {
+    constexpr bool kMasked = decltype(masked_tag)::value;
+    float s[NT][SUB][4];
+    uint32_t top = 0;  // largest V scale
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const uint32_t tile = smem_u32(tiles + u * L::kBytes);
+      uint32_t kc[2 * G], ks[2 * G], kz[2];
+#pragma unroll
+      for (int v = 0; v < 2 * G / 4; ++v) {
+        const uint4 x = lds128(tile + v * 512 + lane * 16), y = lds128(tile + L::kKs + v * 64 + tig * 16);
+        const uint4 w = lds128(tile + L::kVs + v * 64 + tig * 16);
+        kc[4 * v] = x.x; kc[4 * v + 1] = x.y; kc[4 * v + 2] = x.z; kc[4 * v + 3] = x.w;
+        ks[4 * v] = y.x; ks[4 * v + 1] = y.y; ks[4 * v + 2] = y.z; ks[4 * v + 3] = y.w;
+        uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (kMasked) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int p = pos + 16 * u + 8 * ((4 * v + i) / G) + 2 * tig;
+            w4[i] = finite2(w4[i]);
+            if (p >= p1) w4[i] &= 0xFFFF0000u;
+            if (p + 1 >= p1) w4[i] &= 0xFFFFu;
           }
         }
-        acc += __half2float(*reinterpret_cast<const __half*>(tile + L::kKs + L::scale(r, g))) * dot +
-               __half2float(*reinterpret_cast<const __half*>(tile + L::k_min(r, g))) * sum;
+        top = hmax2(top, hmax2(hmax2(w4[0], w4[1]), hmax2(w4[2], w4[3])));
       }
-      sc = acc * a.scale;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) kz[n] = tig < G / 2 ? lds32(tile + L::kKz + (8 * n + gid) * (2 * G) + 4 * tig) : 0u;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, acc[4];
+          mma16816(c, qz[mt][0], qz[mt][1], qz[mt][2], qz[mt][3], kz[n], kz[n]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = c[i] * 3.814697265625e-6f;  // 2^(6 - 24)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const uint32_t w = kc[n * G + g], w8 = w >> 8;
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(d, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w & 0x000F000Fu,
+                     w & 0x00F000F0u);
+            mma16816(d, qa[mt][g][1][0], qa[mt][g][1][1], qa[mt][g][1][2], qa[mt][g][1][3], w8 & 0x000F000Fu,
+                     w8 & 0x00F000F0u);
+            const float s_0 = h_lo(ks[n * G + g]), s_1 = h_hi(ks[n * G + g]);
+            if constexpr (kF32) {
+              acc[0] = fmaf(d[0] + d[2], s_0, acc[0]);
+              acc[1] = fmaf(d[1] + d[3], s_1, acc[1]);
+            } else {
+              acc[0] = fmaf(d[0], s_0, acc[0]);
+              acc[1] = fmaf(d[1], s_1, acc[1]);
+              if constexpr (NT > 1) {
+                acc[2] = fmaf(d[2], s_0, acc[2]);
+                acc[3] = fmaf(d[3], s_1, acc[3]);
+              }
+            }
+          }
+          const int t0 = kF32 ? mt : 2 * mt;
+          s[t0][u][2 * n] = acc[0];
+          s[t0][u][2 * n + 1] = acc[1];
+          if constexpr (!kF32 && NT > 1) {
+            s[t0 + 1][u][2 * n] = acc[2];
+            s[t0 + 1][u][2 * n + 1] = acc[3];
+          }
+        }
+      }
     }
-    float mx = sc;
-    for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float corr = expf(m - mn), pr = tile ? expf(sc - mn) : 0.f;
-    m = mn;
-    l = l * corr + pr;
-    for (int e = 0; e < E; ++e) o[e] *= corr;
-    for (int j = 0; j < 32 && p0 + j < see; ++j) {
-      const float pj = __shfl_sync(0xFFFFFFFFu, pr, j);
-      const uint8_t* tj = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, (unsigned long long)tile, j));
-      if (!tj) continue;
-      const int rj = (p0 + j) % kKv4Tile;
-      for (int e = 0; e < E; ++e) {
-        const int d = lane * E + e;
-        const uint32_t unit = *reinterpret_cast<const uint16_t*>(tj + L::v_unit(rj, d / 4));
-        const float v = fmaf(__half2float(*reinterpret_cast<const __half*>(tj + L::kVs + L::scale(rj, d / 32))),
-                             (float)((unit >> (4 * (d % 4))) & 15u),
-                             __half2float(*reinterpret_cast<const __half*>(tj + L::v_min(rj, d / 32))));
-        o[e] = fmaf(pj, v, o[e]);
+    // reference: running maximum of the row, less the lift
+    top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    top = max(top & 0xFFFFu, top >> 16);
+    const int lift_new = min(lift, 29 - (int)(top >> 10));  // top < 2^(exponent - 14): weight * scale < 2^15
+    bool moved = lift_new != lift;
+    lift = lift_new;
+    float corr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[t][u][i] *= kscale[t];
+          if constexpr (kMasked) {
+            const int p = pos + 16 * u + 8 * (i / 2) + 2 * tig + (i & 1);
+            if (p >= lim[t] || p >= p1) s[t][u][i] = -INFINITY;
+          }
+          mx = fmaxf(mx, s[t][u][i]);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      const bool first = m[t] == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
+      m[t] = fmaxf(m[t], mx);
+      const float r = (m[t] == -INFINITY ? 0.f : m[t]) - (float)lift;
+      corr[t] = first ? 0.f : ex2(ref[t] - r);
+      moved |= r != ref[t];
+      ref[t] = r;
+    }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        l[t] *= corr[t];
+        const float c0 = __shfl_sync(0xFFFFFFFFu, corr[t], 8 * tig), c1 = __shfl_sync(0xFFFFFFFFu, corr[t], 8 * tig + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) oz[t][i] *= (i & 1) ? c1 : c0;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[t][g][j][i] *= (i & 1) ? c1 : c0;
+      }
+    }
+    // weights and values
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const uint32_t tile = smem_u32(tiles + u * L::kBytes);
+      uint32_t vs[2 * G], vz[2];
+#pragma unroll
+      for (int v = 0; v < 2 * G / 4; ++v) {
+        const uint4 y = lds128(tile + L::kVs + v * 64 + tig * 16);
+        vs[4 * v] = y.x; vs[4 * v + 1] = y.y; vs[4 * v + 2] = y.z; vs[4 * v + 3] = y.w;
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        vz[n] = gid < G ? lds32(tile + L::kVz + gid * 32 + n * 16 + tig * 4) : 0u;
+        if constexpr (kMasked) {
+          const int p = pos + 16 * u + 8 * n + 2 * tig;
+          vz[n] = finite2(vz[n]);
+          if (p >= p1) vz[n] &= 0xFFFF0000u;
+          if (p + 1 >= p1) vz[n] &= 0xFFFFu;
+        }
+      }
+      uint32_t wp[NT][2], wl[NT][2];  // weights of positions 2 tig, 2 tig + 1 (+ 8); low parts
+      float w[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[t][i] = ex2(s[t][u][i] - ref[t]);
+          l[t] += w[t][i];
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if constexpr (kF32) split2(w[t][2 * n], w[t][2 * n + 1], wp[t][n], wl[t][n]);
+          else wp[t][n] = pack_h(w[t][2 * n], w[t][2 * n + 1]);
+        }
+        mma16816(oz[t], vz[0], 0u, vz[1], 0u, wp[t][0], wp[t][1]);
+        if constexpr (kF32) mma16816(oz[t], vz[0], 0u, vz[1], 0u, wl[t][0], wl[t][1]);
+      }
+      uint32_t vc[2 * G];
+#pragma unroll
+      for (int v = 0; v < 2 * G / 4; ++v) {
+        const uint4 x = lds128(tile + L::kV + v * 512 + lane * 16);
+        vc[4 * v] = x.x; vc[4 * v + 1] = x.y; vc[4 * v + 2] = x.z; vc[4 * v + 3] = x.w;
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t x0 = vc[2 * g], x1 = vc[2 * g + 1], y0 = x0 >> 8, y1 = x1 >> 8;
+        const uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
+        const uint32_t b0 = y0 & 0x000F000Fu, b1 = y0 & 0x00F000F0u, b2 = y1 & 0x000F000Fu, b3 = y1 & 0x00F000F0u;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint32_t p[2], q[2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t sc = vs[n * G + g];
+            if constexpr (kF32) split2(w[t][2 * n] * h_lo(sc), w[t][2 * n + 1] * h_hi(sc), p[n], q[n]);
+            else p[n] = hmul2(wp[t][n], sc);
+            if constexpr (kMasked) {  // a scale behind the mask may be anything
+              const int at = pos + 16 * u + 8 * n + 2 * tig;
+              const uint32_t keep = (at < lim[t] && at < p1 ? 0xFFFFu : 0u) | (at + 1 < lim[t] && at + 1 < p1 ? 0xFFFF0000u : 0u);
+              p[n] &= keep;
+              if constexpr (kF32) q[n] &= keep;
+            }
+          }
+          mma16816(o[t][g][0], a0, a1, a2, a3, p[0], p[1]);
+          mma16816(o[t][g][1], b0, b1, b2, b3, p[0], p[1]);
+          if constexpr (kF32) {
+            mma16816(o[t][g][0], a0, a1, a2, a3, q[0], q[1]);
+            mma16816(o[t][g][1], b0, b1, b2, b3, q[0], q[1]);
+          }
+        }
+      }
+    }
+  };
+
+  bool alive = true;
+  for (int i = 0; i < mine; ++i) {
+    const int slot = i % kStages, s = s0 + warp + kWarps * i;
+    alive = __all_sync(0xFFFFFFFFu, wait_full(&full[warp][slot], (i / kStages) & 1, a.c.status));
+    if (!alive) break;
+    if (!slot_bad[warp][slot]) {
+      const uint8_t* tiles = ring + slot * kStageBytes;
+      const int pos = s * kStagePos;
+#pragma unroll 1
+      for (int u = 0; u < kTilesPerStage && pos + 16 * u < p1; u += SUB) {
+        const int at = pos + 16 * u;
+        if (at + 16 * SUB <= min(see_all, p1)) step(tiles + u * L::kBytes, at, std::false_type{});
+        else step(tiles + u * L::kBytes, at, std::true_type{});
+      }
+    }
+    __syncwarp();
+    if (i + kStages < mine) issue(i + kStages);
+  }
+  if (!alive) {  // copies still in flight must land before the CTA's shared memory goes
+    for (int i = 0; i < kStages; ++i) wait_full(&full[warp][i], 0, a.c.status), wait_full(&full[warp][i], 1, a.c.status);
+  }
+
+  // ---- merge of the warps' states, in the ring's memory ----
+  __syncthreads();
+  float* ob = reinterpret_cast<float*>(smem);            // [warp][row][D]
+  float* ml = ob + kWarps * kRows * D;                   // [warp][row][2]
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
+    l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 2);
+    if (tig == 0) {
+      ml[(warp * kRows + 8 * t + gid) * 2] = m[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
+      ml[(warp * kRows + 8 * t + gid) * 2 + 1] = l[t];
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      // the minima's part of group g is in the lanes with gid = g
+      const float z0 = __shfl_sync(0xFFFFFFFFu, oz[t][0], 4 * g + tig), z1 = __shfl_sync(0xFFFFFFFFu, oz[t][1], 4 * g + tig);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float* d0 = ob + (warp * kRows + 8 * t + 2 * tig) * D + 32 * g + 4 * gid + 2 * j;
+        *reinterpret_cast<float2*>(d0) =
+            make_float2(fmaf(o[t][g][j][0], 16777216.f, z0), fmaf(o[t][g][j][2], 1048576.f, z0));
+        *reinterpret_cast<float2*>(d0 + D) =
+            make_float2(fmaf(o[t][g][j][1], 16777216.f, z1), fmaf(o[t][g][j][3], 1048576.f, z1));
       }
     }
   }
-  for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-  T* dst = reinterpret_cast<T*>(a.out + row * a.o_row + hq * a.o_head);
-  for (int e = 0; e < E; ++e) dst[lane * E + e] = (T)(l > 0.f || l != l ? o[e] / l : 0.f);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kRows * (D / 8); e += kThreadsA) {
+    const int r = e / (D / 8), w8 = e % (D / 8), row = row0 + r;
+    if (row > last_row) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
+    float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = top == -INFINITY ? 0.f : ex2(ml[(w * kRows + r) * 2] - top);
+      sum = fmaf(f, ml[(w * kRows + r) * 2 + 1], sum);
+      const float* src = ob + (w * kRows + r) * D + 8 * w8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(f, src[i], x[i]);
+    }
+    if (a.n_split > 1) {
+      float* dst = a.part + ((size_t)blockIdx.x * kRows + r) * (D + 4);
+      store8<float>(dst + 4 + 8 * w8, x);
+      if (w8 == 0) *reinterpret_cast<float2*>(dst) = make_float2(top, sum);
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // 0: the row sees nothing
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= inv;
+      store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
+    }
+  }
 }
 
-}  // namespace
-}  // namespace mk
+// Joins the splits of a row: grid (sequence, kv head, row tile), D / 8 threads a row.
+template <int D, class T, int NT>
+__global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
+  constexpr int kRows = 8 * NT;
+  int idx = blockIdx.x;
+  const int rt = a.n_rt - 1 - idx % a.n_rt;
+  idx /= a.n_rt;
+  const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
+  const Kv4Seq seq = kv4_seq(a.b, si);
+  if (!seq.ok) return;
+  const int n_rows = seq.n * a.rep, row0 = rt * kRows, last_row = min(n_rows, row0 + kRows) - 1;
+  const int see_any = max(0, seq.len - seq.n + last_row / a.rep + 1);
+  const int n = max(1, min(a.n_split, (see_any + a.split_len - 1) / a.split_len));
+  for (int e = threadIdx.x; e < kRows * (D / 8); e += 128) {
+    const int r = e / (D / 8), w8 = e % (D / 8), row = row0 + r;
+    if (row > last_row) break;
+    const float* part = a.part + ((size_t)blockIdx.x * a.n_split * kRows + r) * (D + 4);
+    const size_t stride = (size_t)kRows * (D + 4);
+    float top = -INFINITY;
+    for (int s = 0; s < n; ++s) top = fmaxf(top, part[s * stride]);
+    float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n; ++s) {
+      const float* p = part + s * stride;
+      const float f = top == -INFINITY ? 0.f : ex2(p[0] - top);
+      sum = fmaf(f, p[1], sum);
+      float y[8];
+      load8<float>(p + 4 + 8 * w8, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fmaf(f, y[i], x[i]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
+    store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
+  }
+}
 
-using namespace mk;
+struct Plan {
+  int nt, n_rt, n_split, split_len;
+  long long ctas;
+  int64_t part_bytes;
+};
 
-static mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, int32_t n_heads,
-                                 int32_t dtype) {
+// How a call is cut up, from its bounds alone.
+mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dtype, Plan* p) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MK_ERR_CUDA;
+  const long long rows = std::max<long long>(b->max_new, 1) * rep;  // 0: still looks at the spans
+  const int most = c->head_dim == 64 && dtype != 2 ? 4 : 2;
+  p->nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
+  const long long n_rt = (rows + 8 * p->nt - 1) / (8 * p->nt);
+  const long long base = (long long)b->n_seqs * c->n_kv_heads * n_rt;
+  const int unit = MK_KV4_PAGE;
+  const long long pages = (b->max_len + unit - 1) / unit;
+  long long n_split = 1;
+  if (base > 0 && pages > kWarps) {
+    const long long want = (6ll * sms + base - 1) / base;  // about six CTAs per SM
+    n_split = std::max(1ll, std::min(want, pages / kWarps));
+  }
+  const long long per = std::max(1ll, (pages + n_split - 1) / n_split);
+  n_split = std::max(1ll, (pages + per - 1) / per);
+  p->n_rt = (int)n_rt;
+  p->n_split = (int)n_split;
+  p->split_len = (int)std::min<long long>(per * unit, 0x7FFFFFC0);
+  p->ctas = base * n_split;
+  if (p->ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
+  p->part_bytes = n_split > 1 ? p->ctas * 8 * p->nt * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
+  return MK_OK;
+}
+
+// Opt-in to more than 48 KiB of shared memory, once per kernel and device.
+bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready->load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  ready->fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+template <int D, class T, int NT>
+mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  constexpr int kMerge = kWarps * 8 * NT * (D + 2) * 4;
+  constexpr int kSmem = kMerge > kWarps * kStages * kStageBytes ? kMerge : kWarps * kStages * kStageBytes;
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT>), kSmem, &ready)) return MK_ERR_CUDA;
+  attn_few<D, T, NT><<<(unsigned)p.ctas, kThreadsA, kSmem, s>>>(a);
+  if (p.n_split > 1) attn_join<D, T, NT><<<(unsigned)(p.ctas / p.n_split), 128, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
+template <int D, class T>
+mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  if (p.nt == 1) return launch_few<D, T, 1>(a, p, s);
+  if (p.nt == 2) return launch_few<D, T, 2>(a, p, s);
+  if constexpr (D == 64 && sizeof(T) == 2) return launch_few<D, T, 4>(a, p, s);
+  return MK_ERR_UNSUPPORTED;
+}
+
+mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, int32_t n_heads, int32_t dtype) {
   const mk_status st = kv4_check(c, layer, b, dtype);
   if (st != MK_OK) return st;
   if (n_heads < 1 || n_heads % c->n_kv_heads) return MK_ERR_INVALID_ARG;
@@ -122,13 +650,22 @@ static mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_
   return MK_OK;
 }
 
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
 extern "C" mk_status mk_kv4_attention_workspace(const mk_kv4_cache* cache, const mk_kv4_batch* batch, int32_t n_heads,
                                                 int32_t dtype, int64_t* bytes) {
   if (!bytes) return MK_ERR_INVALID_ARG;
-  const mk_status st = check_attention(cache, 0, batch, n_heads, dtype);
+  mk_status st = check_attention(cache, 0, batch, n_heads, dtype);
   if (st != MK_OK) return st;
   *bytes = 0;
-  return MK_OK;
+  if (batch->n_rows == 0) return MK_OK;
+  Plan p;
+  st = plan_few(cache, batch, n_heads / cache->n_kv_heads, dtype, &p);
+  if (st == MK_OK) *bytes = p.part_bytes;
+  return st;
 }
 
 extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
@@ -141,22 +678,24 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
   st = kv4_check_rows(q, dtype, batch->n_rows, n_heads, cache->head_dim, false);
   if (st == MK_OK) st = kv4_check_rows(out, dtype, batch->n_rows, n_heads, cache->head_dim, true);
   if (st != MK_OK) return st;
+  const int rep = n_heads / cache->n_kv_heads;
+  Plan p;
+  st = plan_few(cache, batch, rep, dtype, &p);
+  if (st != MK_OK) return st;
+  if (p.part_bytes > 0 && (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < p.part_bytes))
+    return MK_ERR_INVALID_ARG;
   const int size = dtype == 2 ? 4 : 2;
-  AttnArgs a{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p),
-             q->row_stride * size, q->head_stride * size, out->row_stride * size, out->head_stride * size,
-             layer, n_heads, n_heads / cache->n_kv_heads, scale};
-  const dim3 grid(batch->n_rows, (n_heads + 3) / 4);
+  const AttnArgs a{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p),
+                   q->row_stride * size, q->head_stride * size, out->row_stride * size, out->head_stride * size,
+                   layer, rep, scale * 1.44269504088896341f, p.n_split, p.split_len, p.n_rt,
+                   static_cast<float*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define MK_KV4_ATTN(D, T) attn_simple<D, T><<<grid, 128, 0, s>>>(a)
   if (cache->head_dim == 64) {
-    if (dtype == 0) MK_KV4_ATTN(64, __nv_bfloat16);
-    else if (dtype == 1) MK_KV4_ATTN(64, __half);
-    else MK_KV4_ATTN(64, float);
-  } else {
-    if (dtype == 0) MK_KV4_ATTN(128, __nv_bfloat16);
-    else if (dtype == 1) MK_KV4_ATTN(128, __half);
-    else MK_KV4_ATTN(128, float);
+    if (dtype == 0) return launch_few<64, __nv_bfloat16>(a, p, s);
+    if (dtype == 1) return launch_few<64, __half>(a, p, s);
+    return launch_few<64, float>(a, p, s);
   }
-#undef MK_KV4_ATTN
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  if (dtype == 0) return launch_few<128, __nv_bfloat16>(a, p, s);
+  if (dtype == 1) return launch_few<128, __half>(a, p, s);
+  return launch_few<128, float>(a, p, s);
 }
