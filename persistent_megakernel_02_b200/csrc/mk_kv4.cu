@@ -23,7 +23,9 @@ struct SlotRows {  // a handle's paged cache
 
 template <int D, class T>
 __device__ __forceinline__ char* row_ptr(const BatchRows& b, int which, int, int row, int, int head, int) {
-  return const_cast<char*>(b.base[which]) + row * b.row[which] + head * b.head[which];
+  // (indexing by `which` would put the block in local memory)
+  return const_cast<char*>(which ? b.base[1] : b.base[0]) + row * (which ? b.row[1] : b.row[0]) +
+         head * (which ? b.head[1] : b.head[0]);
 }
 template <int D, class T>
 __device__ __forceinline__ char* row_ptr(const SlotRows& s, int which, int layer, int, int pos, int head, int heads) {
@@ -31,7 +33,7 @@ __device__ __forceinline__ char* row_ptr(const SlotRows& s, int which, int layer
   return s.kv + (((page * heads + head) * 2 + which) * s.PL + pos % s.PL) * (long long)(D * sizeof(T));
 }
 
-// What a CTA works on: one tile of one sequence and kv head.
+// What a warp works on: one tile of one sequence and kv head.
 struct TileJob {
   int tile, first, end;  // tile index; its positions first .. end - 1 are concerned
   int row0;              // batch row of position `first`
@@ -54,7 +56,7 @@ __device__ __forceinline__ TileJob tile_job(const mk_kv4_cache& c, const mk_kv4_
   const Kv4Seq s = kv4_seq(b, lo);
   const int start = s.len - s.n;
   if (!s.ok || start < 0) {
-    if (threadIdx.x == 0) atomicOr(c.status, KV4_BAD_BATCH);
+    if ((threadIdx.x & 31) == 0) atomicOr(c.status, KV4_BAD_BATCH);
     return j;
   }
   const int t = start / kKv4Tile + slot - (s.row0 / kKv4Tile + 2 * lo);
@@ -68,116 +70,177 @@ __device__ __forceinline__ TileJob tile_job(const mk_kv4_cache& c, const mk_kv4_
   return j;
 }
 
-constexpr int kRowThreads = 128;
+constexpr int kRowWarps = 4;  // warps per CTA, each with work of its own
 
-// One CTA quantises one tile of one kv head.  A thread takes 8 neighbouring values of
-// a row (its 4 neighbours share a group).  A tile that is written whole is put
-// together in shared memory and stored with 16-byte stores; one that is not (a single
-// new token) goes out value by value, leaving the other rows as they are.
+// A warp takes the K rows or the V rows (`which`) of one tile of one kv head: a lane has 8
+// neighbouring values of a row (4 neighbouring lanes share a group), and a warp-wide
+// access covers kStep rows.  The place of row r0 + rl in the tile is that of r0 plus that
+// of rl, so only the part of rl is computed at run time.
 template <int D, class T, class Rows>
-__device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head) {
+__device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head,
+                                              int which, uint8_t* image) {
   using L = Kv4<D>;
-  __shared__ __align__(16) uint8_t image[L::kBytes];
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks, kItems = kKv4Tile / kStep;
+  const int lane = threadIdx.x & 31, w = lane % kChunks, rl = lane / kChunks;
   uint8_t* out = kv4_tile<D>(c, j.table, j.layer, head, j.tile);
   if (!out) {
-    if (threadIdx.x == 0) atomicOr(c.status, KV4_BAD_PAGE);
+    if (lane == 0) atomicOr(c.status, KV4_BAD_PAGE);
     return;
   }
   const bool whole = j.end - j.first == kKv4Tile;
-  uint8_t* dst = whole ? image : out;
-  constexpr int kChunks = D / 8, kItems = 2 * kKv4Tile * kChunks;
+  const int skip = j.first - j.tile * kKv4Tile, stop = skip + j.end - j.first;  // the tile's rows concerned
+  // A whole tile's codes and parameters are put together in shared memory and stored with
+  // 16-byte stores: codes of K or of V, 8 D bytes, then scales and minima, 2 D bytes.
+  // Part of a tile (a new token) goes out value by value; the other rows stay as they are.
+  uint8_t* codes_base = whole ? image : out + (which ? L::kV : 0);
+  uint8_t* param_base = whole ? image + 8 * D : out + (which ? L::kVs : L::kKs);
+  uint8_t* codes_at = codes_base + (which ? L::v_unit(rl, 2 * w) - L::kV : L::k_word(rl, w));
+  auto load = [&](Raw8<T> (&raw)[4], int b0) {
 #pragma unroll
-  for (int e0 = 0; e0 < kItems; e0 += kRowThreads) {
-    const int e = e0 + threadIdx.x;
-    const int which = e / (kKv4Tile * kChunks), r = e / kChunks % kKv4Tile, w = e % kChunks;
-    const int pos = j.tile * kKv4Tile + r;
-    const bool in = pos >= j.first && pos < j.end;
-    float x[8];
-    if (in) {
-      load8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + pos - j.first, pos, head, c.n_kv_heads) +
-                   w * 8 * sizeof(T), x);
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      const int r = (b0 + i) * kStep + rl;
+      raw[i] = Raw8<T>{};
+      if (r >= skip && r < stop)
+        raw[i] = load_raw8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head,
+                                            c.n_kv_heads) + w * 8 * sizeof(T));
+    }
+  };
+  Raw8<T> next[4];
+  load(next, 0);
+#pragma unroll 1
+  for (int b0 = 0; b0 < kItems; b0 += 4) {  // four accesses at a time, the next four on their way
+    Raw8<T> raw[4];
+    float2 e[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    for (int i = 0; i < 4; ++i) raw[i] = next[i];
+    if (b0 + 4 < kItems) load(next, b0 + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = extent8(raw[i]);
+    // lane k of a group's quad has the parameters of access k
+    const float lo = quad_scatter_min(e[0].x, e[1].x, e[2].x, e[3].x, lane);
+    const float hi = -quad_scatter_min(e[0].y, e[1].y, e[2].y, e[3].y, lane);
+    const uint32_t mine = kv4_params(lo, hi);
+    const float s = h_lo(mine), inv_mine = s > 0.f ? __frcp_rn(s) : 0.f;
+    {
+      const int r = (b0 + (lane & 3)) * kStep + rl, g = w / 4;
+      if (r >= skip && r < stop) {
+        *reinterpret_cast<uint16_t*>(param_base + L::scale(r, g)) = (uint16_t)mine;
+        *reinterpret_cast<uint16_t*>(param_base + (which ? L::v_min(r, g) - L::kVs : L::k_min(r, g) - L::kKs)) =
+            (uint16_t)(mine >> 16);
+      }
     }
-    __half s, z;
-    const uint32_t codes = kv4_quantise(x, s, z);
-    if (!in) continue;
-    if (which == 0) {
-      *reinterpret_cast<uint32_t*>(dst + L::k_word(r, w)) = codes;
-    } else {
-      *reinterpret_cast<uint16_t*>(dst + L::v_unit(r, 2 * w)) = (uint16_t)codes;
-      *reinterpret_cast<uint16_t*>(dst + L::v_unit(r, 2 * w + 1)) = (uint16_t)(codes >> 16);
-    }
-    if (w % 4 == 0) {
-      *reinterpret_cast<__half*>(dst + (which ? L::kVs : L::kKs) + L::scale(r, w / 4)) = s;
-      *reinterpret_cast<__half*>(dst + (which ? L::v_min(r, w / 4) : L::k_min(r, w / 4))) = z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t params = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) | i);
+      const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, (lane & ~3) | i);
+      float x[8];
+      unpack8(raw[i], x);
+      const uint32_t codes = kv4_codes(x, params, inv);
+      const int r0 = (b0 + i) * kStep, r = r0 + rl;
+      if (r < skip || r >= stop) continue;
+      if (which == 0) {
+        *reinterpret_cast<uint32_t*>(codes_at + L::k_word(r0, 0)) = codes;
+      } else {
+        constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
+        uint8_t* at = codes_at + (L::v_unit(r0, 0) - L::kV);
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)codes;
+        *reinterpret_cast<uint16_t*>(at + kNext) = (uint16_t)(codes >> 16);
+      }
     }
   }
   if (!whole) return;
-  __syncthreads();
-  for (int e = threadIdx.x; e < L::kBytes / 16; e += kRowThreads)
-    reinterpret_cast<uint4*>(out)[e] = reinterpret_cast<const uint4*>(image)[e];
+  __syncwarp();
+#pragma unroll
+  for (int e = lane; e < 8 * D / 16; e += 32)
+    reinterpret_cast<uint4*>(out + (which ? L::kV : 0))[e] = reinterpret_cast<const uint4*>(image)[e];
+  if (lane < 2 * D / 16)
+    reinterpret_cast<uint4*>(out + (which ? L::kVs : L::kKs))[lane] =
+        reinterpret_cast<const uint4*>(image + 8 * D)[lane];
 }
 
-// One CTA reads one tile of one kv head: the tile comes in with 16-byte loads, and a
-// thread puts out 8 neighbouring values of a row.
+// The way back: codes and parameters come in with 16-byte loads, and a lane puts out 8
+// neighbouring values of a row.
 template <int D, class T, class Rows>
-__device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head) {
+__device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head,
+                                          int which, uint8_t* image) {
   using L = Kv4<D>;
-  __shared__ __align__(16) uint8_t image[L::kBytes];
+  constexpr int kChunks = D / 8, kStep = 32 / kChunks, kItems = kKv4Tile / kStep;
+  const int lane = threadIdx.x & 31, w = lane % kChunks, rl = lane / kChunks;
   const uint8_t* src = kv4_tile<D>(c, j.table, j.layer, head, j.tile);
   if (!src) {
-    if (threadIdx.x == 0) atomicOr(c.status, KV4_BAD_PAGE);
+    if (lane == 0) atomicOr(c.status, KV4_BAD_PAGE);
     return;
   }
-  for (int e = threadIdx.x; e < L::kBytes / 16; e += kRowThreads)
-    reinterpret_cast<uint4*>(image)[e] = reinterpret_cast<const uint4*>(src)[e];
-  __syncthreads();
-  constexpr int kChunks = D / 8, kItems = 2 * kKv4Tile * kChunks;
 #pragma unroll
-  for (int e0 = 0; e0 < kItems; e0 += kRowThreads) {
-    const int e = e0 + threadIdx.x;
-    const int which = e / (kKv4Tile * kChunks), r = e / kChunks % kKv4Tile, w = e % kChunks;
-    const int pos = j.tile * kKv4Tile + r;
-    if (pos < j.first || pos >= j.end) continue;
+  for (int e = lane; e < 8 * D / 16; e += 32)
+    reinterpret_cast<uint4*>(image)[e] = reinterpret_cast<const uint4*>(src + (which ? L::kV : 0))[e];
+  if (lane < 2 * D / 16)
+    reinterpret_cast<uint4*>(image + 8 * D)[lane] =
+        reinterpret_cast<const uint4*>(src + (which ? L::kVs : L::kKs))[lane];
+  __syncwarp();
+  const uint8_t* codes_at = image + (which ? L::v_unit(rl, 2 * w) - L::kV : L::k_word(rl, w));
+  const uint8_t* scale_at = image + 8 * D + L::scale(rl, w / 4);
+  const uint8_t* min_at = image + 8 * D + (which ? L::v_min(rl, w / 4) - L::kVs : L::k_min(rl, w / 4) - L::kKs);
+  const int skip = j.first - j.tile * kKv4Tile;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int r = i * kStep + rl;
     uint32_t codes;
     if (which == 0) {
-      codes = *reinterpret_cast<const uint32_t*>(image + L::k_word(r, w));
+      codes = *reinterpret_cast<const uint32_t*>(codes_at + L::k_word(i * kStep, 0));
     } else {
-      codes = *reinterpret_cast<const uint16_t*>(image + L::v_unit(r, 2 * w)) |
-              (uint32_t)*reinterpret_cast<const uint16_t*>(image + L::v_unit(r, 2 * w + 1)) << 16;
+      constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
+      const uint8_t* at = codes_at + (L::v_unit(i * kStep, 0) - L::kV);
+      codes = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + kNext) << 16;
     }
-    const float s = __half2float(*reinterpret_cast<const __half*>(image + (which ? L::kVs : L::kKs) + L::scale(r, w / 4)));
-    const float z = __half2float(*reinterpret_cast<const __half*>(image + (which ? L::v_min(r, w / 4) : L::k_min(r, w / 4))));
+    const uint32_t params =
+        *reinterpret_cast<const uint16_t*>(scale_at + L::scale(i * kStep, 0)) |
+        (uint32_t)*reinterpret_cast<const uint16_t*>(
+            min_at + (which ? L::v_min(i * kStep, 0) - L::kVz : L::k_min(i * kStep, 0) - L::kKz)) << 16;
     float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(s, (float)((codes >> (4 * i)) & 15u), z);
-    store8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + pos - j.first, pos, head, c.n_kv_heads) + w * 8 * sizeof(T), x);
+    kv4_values(codes, h_lo(params), h_hi(params), x);
+    if (r >= skip && r < skip + j.end - j.first)
+      store8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head, c.n_kv_heads) +
+                    w * 8 * sizeof(T), x);
   }
 }
 
-template <int D, class T, bool WRITE>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(mk_kv4_cache c, int layer, mk_kv4_batch b, BatchRows rows) {
-  const TileJob j = tile_job(c, b, layer, blockIdx.x);
-  if (!j.ok) return;
-  if (WRITE) quantise_tile<D, T>(c, j, rows, blockIdx.y);
-  else read_tile<D, T>(c, j, rows, blockIdx.y);
+template <int D, class T, bool WRITE, class Rows>
+__device__ __forceinline__ void do_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head, int which) {
+  __shared__ __align__(16) uint8_t image[kRowWarps][10 * D];
+  if (WRITE) quantise_tile<D, T>(c, j, rows, head, which, image[threadIdx.x >> 5]);
+  else read_tile<D, T>(c, j, rows, head, which, image[threadIdx.x >> 5]);
 }
 
-// Positions start .. start + n - 1 of a handle's slot, every layer: grid (tiles, kv heads, layers).
+// Warp g of the grid: kv head g % n_kv_heads, then K or V, then the slot, so neighbouring
+// warps are at neighbouring heads of the same rows.
 template <int D, class T, bool WRITE>
-__global__ void __launch_bounds__(kRowThreads)
-    slot_kernel(mk_kv4_cache c, SlotRows rows, const int32_t* table_row, int start, int n) {
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
+    rows_kernel(mk_kv4_cache c, int layer, mk_kv4_batch b, BatchRows rows, int n_slots) {
+  const long long g = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const int head = (int)(g % c.n_kv_heads), which = (int)(g / c.n_kv_heads & 1);
+  const int slot = (int)(g / (2 * c.n_kv_heads));
+  if (slot >= n_slots) return;
+  const TileJob j = tile_job(c, b, layer, slot);
+  if (j.ok) do_tile<D, T, WRITE>(c, j, rows, head, which);
+}
+
+// Positions start .. start + n - 1 of a handle's slot: warps over (tile, K or V, kv head),
+// grid.y over the layers.
+template <int D, class T, bool WRITE>
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
+    slot_kernel(mk_kv4_cache c, SlotRows rows, const int32_t* table_row, int start, int n, int n_tiles) {
+  const int g = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const int head = g % c.n_kv_heads, which = g / c.n_kv_heads & 1, t = g / (2 * c.n_kv_heads);
+  if (t >= n_tiles) return;
   TileJob j;
-  j.tile = start / kKv4Tile + blockIdx.x;
+  j.tile = start / kKv4Tile + t;
   j.first = max(start, j.tile * kKv4Tile);
   j.end = min(start + n, (j.tile + 1) * kKv4Tile);
   j.row0 = 0;
-  j.layer = blockIdx.z;
+  j.layer = blockIdx.y;
   j.table = table_row;
-  if (WRITE) quantise_tile<D, T>(c, j, rows, blockIdx.y);
-  else read_tile<D, T>(c, j, rows, blockIdx.y);
+  do_tile<D, T, WRITE>(c, j, rows, head, which);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -202,10 +265,10 @@ mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, 
     rows.head[i] = kv[i]->head_stride * size;
   }
   const long long slots = b->n_rows / kKv4Tile + 2ll * b->n_seqs;
-  if (slots > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)slots, c->n_kv_heads);
+  const long long ctas = (2 * slots * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
+  if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define MK_KV4_ROWS(D, T) rows_kernel<D, T, WRITE><<<grid, kRowThreads, 0, s>>>(*c, layer, *b, rows)
+#define MK_KV4_ROWS(D, T) rows_kernel<D, T, WRITE><<<(unsigned)ctas, 32 * kRowWarps, 0, s>>>(*c, layer, *b, rows, (int)slots)
   if (c->head_dim == 64) {
     if (dtype == 0) MK_KV4_ROWS(64, __nv_bfloat16);
     else if (dtype == 1) MK_KV4_ROWS(64, __half);
@@ -256,10 +319,13 @@ mk_status kv4_check_rows(const mk_kv4_rows* r, int32_t dtype, int64_t rows, int3
 mk_status kv4_slot(bool write, const mk_kv4_cache* c, void* kv, const int* slot_table, int n_phys_pages, int PL,
                    bool fp16, const int32_t* table_row, int start, int n, cudaStream_t s) {
   const SlotRows rows{static_cast<char*>(kv), slot_table, n_phys_pages, PL};
-  const dim3 grid((start + n - 1) / kKv4Tile - start / kKv4Tile + 1, c->n_kv_heads, c->n_layers);
-#define MK_KV4_SLOT(D, T)                                                                          \
-  (write ? slot_kernel<D, T, true><<<grid, kRowThreads, 0, s>>>(*c, rows, table_row, start, n)     \
-         : slot_kernel<D, T, false><<<grid, kRowThreads, 0, s>>>(*c, rows, table_row, start, n))
+  const int n_tiles = (start + n - 1) / kKv4Tile - start / kKv4Tile + 1;
+  const long long ctas = (2ll * n_tiles * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
+  if (ctas * kRowWarps > 0x7FFFFFFF || c->n_layers > 65535) return MK_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)ctas, c->n_layers);
+#define MK_KV4_SLOT(D, T)                                                                                        \
+  (write ? slot_kernel<D, T, true><<<grid, 32 * kRowWarps, 0, s>>>(*c, rows, table_row, start, n, n_tiles)       \
+         : slot_kernel<D, T, false><<<grid, 32 * kRowWarps, 0, s>>>(*c, rows, table_row, start, n, n_tiles))
   if (c->head_dim == 64) {
     if (fp16) MK_KV4_SLOT(64, __half);
     else MK_KV4_SLOT(64, __nv_bfloat16);

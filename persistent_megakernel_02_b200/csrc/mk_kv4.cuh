@@ -88,24 +88,34 @@ __device__ __forceinline__ uint8_t* kv4_tile(const mk_kv4_cache& c, const int32_
 
 // ---- rows of 16-bit or 32-bit values ----
 template <class T>
-__device__ __forceinline__ void load8(const void* p, float (&x)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const void* p, float (&x)[8]) {
-  const float4 a = __ldg(static_cast<const float4*>(p)), b = __ldg(static_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+struct Raw8 {  // 8 values as they are in memory
+  uint4 v[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw8<T> load_raw8(const void* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ldnc16(static_cast<const uint4*>(p) + i);
+  return r;
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const void* p, float (&x)[8]) {
-  const uint4 a = ldnc16(p);
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint4 a = r.v[0];
   x[0] = bf_lo(a.x); x[1] = bf_hi(a.x); x[2] = bf_lo(a.y); x[3] = bf_hi(a.y);
   x[4] = bf_lo(a.z); x[5] = bf_hi(a.z); x[6] = bf_lo(a.w); x[7] = bf_hi(a.w);
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const void* p, float (&x)[8]) {
-  const uint4 a = ldnc16(p);
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&x)[8]) {
+  const uint4 a = r.v[0];
   x[0] = h_lo(a.x); x[1] = h_hi(a.x); x[2] = h_lo(a.y); x[3] = h_hi(a.y);
   x[4] = h_lo(a.z); x[5] = h_hi(a.z); x[6] = h_lo(a.w); x[7] = h_hi(a.w);
+}
+template <class T>
+__device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
+  unpack8(load_raw8<T>(p), x);
 }
 __device__ __forceinline__ uint32_t pack_bf(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -141,58 +151,109 @@ __device__ __forceinline__ int cmp_sum(float a, float b, float x) {
   return s > x ? 1 : s < x ? -1 : e > 0.f ? 1 : e < 0.f ? -1 : 0;
 }
 
-// Codes of this thread's 8 values (4 bits each, value i at bits 4 i) and the group's
-// scale and minimum; the 4 threads of a group are neighbouring lanes of one aligned
-// quad, and every lane of the warp calls.  A group that holds anything beyond
-// +-2^15, an infinity or a NaN gets NaN parameters, so it reads back as NaN.
-// Everything is decided exactly as in real arithmetic: where the fast quotient is
-// within its error of a border between two codes, the border z + (k + 1/2) s is
-// compared with x through an exact sum.
-__device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], __half& s_out, __half& z_out) {
-  float lo = x[0], hi = x[0];
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad |= !(fabsf(x[i]) <= 32768.f);
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-    bad |= __shfl_xor_sync(0xFFFFFFFFu, (int)bad, o) != 0;
-  }
-  if (bad) {
-    s_out = z_out = __ushort_as_half((unsigned short)0x7FFF);
-    return 0u;
-  }
+// minimum and maximum that keep a NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// {minimum, -maximum} of 8 values, NaN where one is; 16-bit types in packed pairs
+__device__ __forceinline__ float2 extent8(const Raw8<float>& r) {
+  float x[8];
+  unpack8(r, x);
+  return make_float2(
+      min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7]))),
+      -max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7]))));
+}
+template <class H2, class T>
+__device__ __forceinline__ float2 extent8_packed(const Raw8<T>& r) {
+  const H2* h = reinterpret_cast<const H2*>(&r.v[0]);
+  const H2 lo = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
+  const H2 hi = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+  return make_float2(min_nan((float)lo.x, (float)lo.y), -max_nan((float)hi.x, (float)hi.y));
+}
+__device__ __forceinline__ float2 extent8(const Raw8<__nv_bfloat16>& r) { return extent8_packed<__nv_bfloat162>(r); }
+__device__ __forceinline__ float2 extent8(const Raw8<__half>& r) { return extent8_packed<__half2>(r); }
+
+// Scale and minimum of a group with these extremes (low 16 bits the scale).  A group
+// that holds anything beyond +-2^15, an infinity or a NaN gets NaN for both, so it
+// reads back as NaN.
+__device__ __forceinline__ uint32_t kv4_params(float lo, float hi) {
+  if (!(lo >= -32768.f && hi <= 32768.f)) return 0x7FFF7FFFu;
   const __half zh = __float2half_rd(lo);
   const float z = __half2float(zh);
-  // smallest fp16 s with z + 15 s >= max: a guess within one step, then the exact test
-  unsigned short sb = __half_as_ushort(__float2half_ru((hi - z) * (1.0f / 15.0f)));
-  auto covers = [&](unsigned short b) {
-    return cmp_sum(15.0f * __half2float(__ushort_as_half(b)), z, hi) >= 0;
-  };
-  if (!covers(sb)) ++sb;
-  else if (sb != 0 && covers((unsigned short)(sb - 1))) --sb;
-  const float s = __half2float(__ushort_as_half(sb));
-  const float inv = s > 0.f ? 1.0f / s : 0.f;
+  // smallest fp16 s with z + 15 s >= max: rounded up from just below the quotient it is
+  // that one or the one before, which the exact sum tells
+  uint32_t sb = __half_as_ushort(__float2half_ru((hi - z) * (0.9999995f / 15.0f)));
+  if (cmp_sum(15.0f * __half2float(__ushort_as_half((unsigned short)sb)), z, hi) < 0) ++sb;
+  return sb | (uint32_t)__half_as_ushort(zh) << 16;
+}
+
+constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer, kept in the low bits
+
+// The code of x next to a border between two codes, as in real arithmetic: the border
+// z + (k + 1/2) s is compared with x through an exact sum; ties go to the even code.
+__device__ __forceinline__ uint32_t kv4_code_exact(float x, float s, float z, float inv) {
+  const float t = (x - z) * inv;  // within 2^-18 of the quotient
+  float n = (t + kRound) - kRound;
+  if (fabsf(t - n) > 0.5f - 7.6e-6f) {
+    const float k = t > n ? n : n - 1.0f;
+    const int c = cmp_sum((k + 0.5f) * s, z, x);  // border - x
+    n = c < 0 ? k + 1.0f : c > 0 ? k : (((int)k & 1) ? k + 1.0f : k);
+  }
+  return (uint32_t)(int)n;
+}
+// (a call of its own: inlined for every 8 values it made the kernel miss the instruction
+// cache, a third of its stalls)
+static __device__ __noinline__ uint32_t kv4_codes_exact(float x0, float x1, float x2, float x3, float x4, float x5,
+                                                        float x6, float x7, float s, float z, float inv) {
+  return kv4_code_exact(x0, s, z, inv) | kv4_code_exact(x1, s, z, inv) << 4 | kv4_code_exact(x2, s, z, inv) << 8 |
+         kv4_code_exact(x3, s, z, inv) << 12 | kv4_code_exact(x4, s, z, inv) << 16 |
+         kv4_code_exact(x5, s, z, inv) << 20 | kv4_code_exact(x6, s, z, inv) << 24 | kv4_code_exact(x7, s, z, inv) << 28;
+}
+
+// Codes of 8 values of a group (4 bits each, value i at bits 4 i); inv is 1 / s to 2^-23,
+// 0 where s is 0 or NaN.  Integers come through the low bits of a float: the
+// conversion instructions run at an eighth of the rate.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], uint32_t params, float inv) {
+  const float z = h_hi(params), zi = -z * inv;
+  if (inv == 0.f) return 0u;  // all equal, or NaN
   uint32_t codes = 0;
+  float off = 0.f;  // largest distance from an integer
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = (x[i] - z) * inv;  // within 2^-18 of the quotient (t < 16)
-    float n = rintf(t);
-    if (fabsf(t - n) > 0.5f - 7.6e-6f) {
-      const float k = t > n ? n : n - 1.0f;
-      const int c = cmp_sum((k + 0.5f) * s, z, x[i]);  // border - x
-      n = c < 0 ? k + 1.0f : c > 0 ? k : (((int)k & 1) ? k + 1.0f : k);
-    }
-    codes |= (uint32_t)(int)n << (4 * i);
+    const float t = fmaf(x[i], inv, zi), n = t + kRound;
+    off = fmaxf(off, fabsf(t - (n - kRound)));
+    codes += (__float_as_uint(n) - __float_as_uint(kRound)) << (4 * i);
   }
-  s_out = __ushort_as_half(sb);
-  z_out = zh;
+  // t is off by 2^-24 of z / s (rounded once) and, t being below 16, by 16 (2^-23 + 2^-24)
+  if (off > 0.5f - fmaf(fabsf(zi), 1.2e-7f, 3.9e-6f))  // some value is next to a border
+    codes = kv4_codes_exact(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], h_lo(params), z, inv);
   return codes;
+}
+
+// What a lane sends and keeps when four items, one quarter of each in every lane of a
+// quad, are reduced so that lane k of the quad ends up with item k.
+__device__ __forceinline__ float quad_scatter_min(float e0, float e1, float e2, float e3, int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  const float a = min_nan(odd ? e1 : e0, __shfl_xor_sync(0xFFFFFFFFu, odd ? e0 : e1, 1));
+  const float b = min_nan(odd ? e3 : e2, __shfl_xor_sync(0xFFFFFFFFu, odd ? e2 : e3, 1));
+  return min_nan(high ? b : a, __shfl_xor_sync(0xFFFFFFFFu, high ? a : b, 2));
+}
+
+// the 8 values of a K word (or of two V units) of a group with scale s and minimum z
+__device__ __forceinline__ void kv4_values(uint32_t codes, float s, float z, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = __uint_as_float((codes >> (4 * i) & 15u) | __float_as_uint(8388608.0f)) - 8388608.0f;
+    x[i] = fmaf(s, c, z);
+  }
 }
 
 }  // namespace mk
