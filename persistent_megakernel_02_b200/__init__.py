@@ -399,7 +399,7 @@ class Megakernel:
                              "cache's device with a row for the sequence")
         if cache.device.index != self._device:
             raise MkError(1, f"{what}: the cache is not on the handle's device ({self._device})")
-        _check(fn(self._h, slot, start, n, cache._ref, table.data_ptr() + 4 * int(table.shape[1]) * seq,
+        _check(fn(self._h, slot, start, n, cache._struct, table.data_ptr() + 4 * int(table.shape[1]) * seq,
                   int(table.shape[1]), _stream_handle(stream)), what)
 
     def park(self, slot, n, cache, seq, start=0, block_table=None, stream=None):
@@ -451,4 +451,10 @@ class Megakernel:
             pass
 
 
-from .kv4 import Kv4Batch, Kv4Cache  # noqa: E402  (the module uses the names above)
+def __getattr__(name):
+    """Kv4Cache and Kv4Batch on first use: their module needs torch at import."""
+    if name in ("Kv4Cache", "Kv4Batch"):
+        from . import kv4
+
+        return getattr(kv4, name)
+    raise AttributeError(name)

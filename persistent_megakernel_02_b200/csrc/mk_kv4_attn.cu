@@ -35,7 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreadsA = 32 * kWarps;
 constexpr int kStageBytes = 5120;
-constexpr int kStages = 3;  // ring depth per warp
+constexpr int kStages = 2;  // ring depth per warp
+constexpr int kHead = 4;    // log2 of what a weight may pass the reference by
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 struct AttnArgs {
@@ -51,13 +52,22 @@ struct AttnArgs {
   float* part;             // [seq][kv head][row tile][split][8 NT][D + 2]
 };
 
+// c += A B (16 x 16 by 16 x 8), and the same from zero
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint4 lds_u4(const uint8_t* p) { return lds128(smem_u32(p)); }
+__device__ __forceinline__ uint32_t lds_u1(const uint8_t* p) { return lds32(smem_u32(p)); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -104,7 +114,7 @@ __device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32
 // 32-bit calls split queries and weights into two fp16 parts: the queries' low parts
 // are rows 8..15 of the same mma, the weights' take a second one.
 template <int D, class T, int NT>
-__global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const AttnArgs a) {
   using L = Kv4<D>;
   constexpr int G = L::G;
   constexpr bool kF32 = sizeof(T) == 4;
@@ -112,7 +122,7 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   constexpr int kTilesPerStage = kStageBytes / L::kBytes;
   constexpr int kStagePos = kTilesPerStage * kKv4Tile;  // positions of a stage
   constexpr int kStagesPerPage = MK_KV4_PAGE / kStagePos;
-  constexpr int SUB = NT >= 4 ? 2 : kTilesPerStage;     // tiles per softmax step
+  constexpr int SUB = 2;                                // tiles per softmax step
   constexpr int kRows = 8 * NT;
 
   extern __shared__ __align__(16) uint8_t smem[];
@@ -127,6 +137,15 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   const int rt = a.n_rt - 1 - idx % a.n_rt;  // the tiles that see most come first
   idx /= a.n_rt;
   const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
+  asm volatile("griddepcontrol.launch_dependents;");
+  // the first page ids are loaded together with the lengths, which only bound them
+  const int p0 = split * a.split_len, s0 = p0 / kStagePos;
+  const int32_t* table = a.b.block_table + (size_t)si * a.b.max_pages;
+  int page_id = 0;  // lane i: page of this warp's stage (32 k + i)
+  {
+    const int page = (s0 + warp + kWarps * lane) / kStagesPerPage;
+    if (page < a.b.max_pages && kWarps * lane * kStagePos < a.split_len) page_id = table[page];
+  }
   const Kv4Seq seq = kv4_seq(a.b, si);
   if (!seq.ok) {
     if (threadIdx.x == 0) atomicOr(a.c.status, KV4_BAD_BATCH);
@@ -138,16 +157,14 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   const int last_row = min(n_rows, row0 + kRows) - 1;
   const int see_all = start + row0 / a.rep + 1;                // positions every row of the tile sees
   const int see_any = max(0, start + last_row / a.rep + 1);    // positions some row sees
-  const int p0 = split * a.split_len, p1 = min(see_any, p0 + a.split_len);
+  const int p1 = min(see_any, p0 + a.split_len);
   if (p0 >= p1 && split > 0) return;  // the merge takes only the splits that hold something
-  const int32_t* table = a.b.block_table + (size_t)si * a.b.max_pages;
 
   // ---- ring of bulk copies: this warp's stage i is stage s0 + warp + kWarps i ----
-  const int s0 = p0 / kStagePos, n_stages = p0 < p1 ? (p1 - 1) / kStagePos - s0 + 1 : 0;
+  const int n_stages = p0 < p1 ? (p1 - 1) / kStagePos - s0 + 1 : 0;
   const int mine = n_stages > warp ? (n_stages - warp - 1) / kWarps + 1 : 0;
-  int page_id = 0;  // lane i: page of this warp's stage (32 k + i)
   auto issue = [&](int i) {  // every lane calls
-    if ((i & 31) == 0) {
+    if (i > 0 && (i & 31) == 0) {
       const int j = i + lane;
       page_id = j < mine ? table[(s0 + warp + kWarps * j) / kStagesPerPage] : 0;
     }
@@ -177,7 +194,12 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   for (int i = 0; i < kStages && i < mine; ++i) issue(i);
 
   // ---- queries: operand order of the codes, scaled by a power of two per row ----
-  uint32_t qa[MT][G][2][4];  // [16 rows][group][k16 step][a0..a3]
+  // [16 rows][group][k16 step][a0..a3].  With 8 rows of 16-bit queries rows 8..15 of the
+  // operand would be idle: there it holds both steps, step 0 in rows 0..7 and step 1 in
+  // rows 8..15, each product taken from its own half (half the registers, and no zeros to
+  // be moved into place).
+  constexpr bool kBoth = !kF32 && NT == 1;
+  uint32_t qa[MT][G][kBoth ? 1 : 2][4];
   uint32_t qz[MT][4];        // sums over the groups, for the minima
   float kscale[NT];          // score = kscale * accumulated
   int lim[NT];               // positions the row sees
@@ -210,7 +232,9 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
     // with an infinity keep theirs)
     const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
     const float up = __uint_as_float((uint32_t)(127 + max(e, -126)) << 23);
-    kscale[t] = a.scale_log2 * 16777216.f / up;
+    const float signed_up = a.scale_log2 < 0.f ? -up : up;
+    // (never zero: it multiplies the -inf of masked positions)
+    kscale[t] = fmaxf(fabsf(a.scale_log2) * 16777216.f / up, 1e-37f);
     lim[t] = live ? start + r / a.rep + 1 : 0;
     float sums[G];
 #pragma unroll
@@ -218,7 +242,7 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[g][i] *= up;
+        x[g][i] *= signed_up;
         sum += x[g][i];
       }
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
@@ -235,10 +259,12 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
           qa[t][g][st][1] = l0;
           qa[t][g][st][2] = h1;
           qa[t][g][st][3] = l1;
+        } else if constexpr (kBoth) {
+          qa[0][g][0][st] = h0;
+          qa[0][g][0][2 + st] = h1;
         } else {
           qa[t / 2][g][st][t & 1] = h0;
           qa[t / 2][g][st][2 + (t & 1)] = h1;
-          if constexpr (NT == 1) qa[0][g][st][1] = qa[0][g][st][3] = 0u;
         }
       }
     }
@@ -256,14 +282,19 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
       qz[t / 2][t & 1] = zh;
       qz[t / 2][2 + (t & 1)] = zl;
     }
+    if constexpr (kBoth) qz[0][1] = zh, qz[0][3] = zl;  // idle rows
   }
 
-  float o[NT][G][2][4], oz[NT][4], m[NT], l[NT], ref[NT];
-  int lift = 14;  // weights are scaled by 2^lift: 14, or less where scales are large
+  // oz: row g the minima's part of group g, row G (operand of ones) the sum of the weights
+  float o[NT][G][2][4], oz[NT][4], m[NT], ref[NT];
+  // weights are scaled by 2^lift: 14 - kHead, or less where scales are large; cap: the
+  // largest scale this lift allows (a pair of halves)
+  int lift = 14 - kHead;
+  uint32_t cap = 0x3FFF3FFFu;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = ref[t] = -INFINITY;
-    l[t] = 0.f;
+    m[t] = -INFINITY;
+    ref[t] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) oz[t][i] = 0.f;
 #pragma unroll
@@ -281,12 +312,12 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
     uint32_t top = 0;  // largest V scale
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      const uint32_t tile = smem_u32(tiles + u * L::kBytes);
+      const uint8_t* tile = tiles + u * L::kBytes;
       uint32_t kc[2 * G], ks[2 * G], kz[2];
 #pragma unroll
       for (int v = 0; v < 2 * G / 4; ++v) {
-        const uint4 x = lds128(tile + v * 512 + lane * 16), y = lds128(tile + L::kKs + v * 64 + tig * 16);
-        const uint4 w = lds128(tile + L::kVs + v * 64 + tig * 16);
+        const uint4 x = lds_u4(tile + v * 512 + lane * 16), y = lds_u4(tile + L::kKs + v * 64 + tig * 16);
+        const uint4 w = lds_u4(tile + L::kVs + v * 64 + tig * 16);
         kc[4 * v] = x.x; kc[4 * v + 1] = x.y; kc[4 * v + 2] = x.z; kc[4 * v + 3] = x.w;
         ks[4 * v] = y.x; ks[4 * v + 1] = y.y; ks[4 * v + 2] = y.z; ks[4 * v + 3] = y.w;
         uint32_t w4[4] = {w.x, w.y, w.z, w.w};
@@ -302,82 +333,89 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
         top = hmax2(top, hmax2(hmax2(w4[0], w4[1]), hmax2(w4[2], w4[3])));
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n) kz[n] = tig < G / 2 ? lds32(tile + L::kKz + (8 * n + gid) * (2 * G) + 4 * tig) : 0u;
+      for (int n = 0; n < 2; ++n) kz[n] = tig < G / 2 ? lds_u1(tile + L::kKz + (8 * n + gid) * (2 * G) + 4 * tig) : 0u;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f}, acc[4];
-          mma16816(c, qz[mt][0], qz[mt][1], qz[mt][2], qz[mt][3], kz[n], kz[n]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = c[i] * 3.814697265625e-6f;  // 2^(6 - 24)
+          float c[4];
+          mma16816_zero(c, qz[mt][0], qz[mt][1], qz[mt][2], qz[mt][3], kz[n], kz[n]);
+          const float2 unit = make_float2(3.814697265625e-6f, 3.814697265625e-6f);  // 2^(6 - 24)
+          float2 acc0 = __fmul2_rn(make_float2(c[0], c[1]), unit), acc1;  // rows 0..7, 8..15
+          if constexpr (!kF32 && NT > 1) acc1 = __fmul2_rn(make_float2(c[2], c[3]), unit);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const uint32_t w = kc[n * G + g], w8 = w >> 8;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(d, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w & 0x000F000Fu,
-                     w & 0x00F000F0u);
-            mma16816(d, qa[mt][g][1][0], qa[mt][g][1][1], qa[mt][g][1][2], qa[mt][g][1][3], w8 & 0x000F000Fu,
-                     w8 & 0x00F000F0u);
-            const float s_0 = h_lo(ks[n * G + g]), s_1 = h_hi(ks[n * G + g]);
-            if constexpr (kF32) {
-              acc[0] = fmaf(d[0] + d[2], s_0, acc[0]);
-              acc[1] = fmaf(d[1] + d[3], s_1, acc[1]);
+            const float2 sc = make_float2(h_lo(ks[n * G + g]), h_hi(ks[n * G + g]));
+            float d[4];
+            mma16816_zero(d, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w & 0x000F000Fu,
+                          w & 0x00F000F0u);
+            float2 d0, d1;
+            if constexpr (kBoth) {
+              float e[4];
+              mma16816_zero(e, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w8 & 0x000F000Fu,
+                            w8 & 0x00F000F0u);
+              d0 = __fadd2_rn(make_float2(d[0], d[1]), make_float2(e[2], e[3]));
             } else {
-              acc[0] = fmaf(d[0], s_0, acc[0]);
-              acc[1] = fmaf(d[1], s_1, acc[1]);
-              if constexpr (NT > 1) {
-                acc[2] = fmaf(d[2], s_0, acc[2]);
-                acc[3] = fmaf(d[3], s_1, acc[3]);
-              }
+              mma16816(d, qa[mt][g][1][0], qa[mt][g][1][1], qa[mt][g][1][2], qa[mt][g][1][3], w8 & 0x000F000Fu,
+                       w8 & 0x00F000F0u);
+              d0 = make_float2(d[0], d[1]);
+              d1 = make_float2(d[2], d[3]);
+              if constexpr (kF32) d0 = __fadd2_rn(d0, d1);
             }
+            acc0 = __ffma2_rn(d0, sc, acc0);
+            if constexpr (!kF32 && NT > 1) acc1 = __ffma2_rn(d1, sc, acc1);
           }
           const int t0 = kF32 ? mt : 2 * mt;
-          s[t0][u][2 * n] = acc[0];
-          s[t0][u][2 * n + 1] = acc[1];
+          s[t0][u][2 * n] = acc0.x;
+          s[t0][u][2 * n + 1] = acc0.y;
           if constexpr (!kF32 && NT > 1) {
-            s[t0 + 1][u][2 * n] = acc[2];
-            s[t0 + 1][u][2 * n + 1] = acc[3];
+            s[t0 + 1][u][2 * n] = acc1.x;
+            s[t0 + 1][u][2 * n + 1] = acc1.y;
           }
         }
       }
     }
-    // reference: running maximum of the row, less the lift
-    top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    top = max(top & 0xFFFFu, top >> 16);
-    const int lift_new = min(lift, 29 - (int)(top >> 10));  // top < 2^(exponent - 14): weight * scale < 2^15
-    bool moved = lift_new != lift;
-    lift = lift_new;
-    float corr[NT];
+    // The weights are 2^(score - ref), ref = m - lift with m the row's maximum when it was
+    // last moved: it moves only when a score passes m by more than kHead (or a scale the
+    // largest one allowed so far), so most steps need one vote and no shuffle.
+    bool over = hmax2(top, cap) != cap;
+    float mx[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float mx = -INFINITY;
+      float r[SUB];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < SUB; ++u) {
+        if constexpr (kMasked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[t][u][i] *= kscale[t];
-          if constexpr (kMasked) {
+          for (int i = 0; i < 4; ++i) {
             const int p = pos + 16 * u + 8 * (i / 2) + 2 * tig + (i & 1);
             if (p >= lim[t] || p >= p1) s[t][u][i] = -INFINITY;
           }
-          mx = fmaxf(mx, s[t][u][i]);
         }
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      const bool first = m[t] == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
-      m[t] = fmaxf(m[t], mx);
-      const float r = (m[t] == -INFINITY ? 0.f : m[t]) - (float)lift;
-      corr[t] = first ? 0.f : ex2(ref[t] - r);
-      moved |= r != ref[t];
-      ref[t] = r;
+        r[u] = fmaxf(fmaxf(s[t][u][0], s[t][u][1]), fmaxf(s[t][u][2], s[t][u][3]));
+      }
+#pragma unroll
+      for (int u = 1; u < SUB; ++u) r[0] = fmaxf(r[0], r[u]);
+      mx[t] = r[0] * kscale[t];
+      over |= mx[t] > m[t] + kHead;
     }
-    if (__any_sync(0xFFFFFFFFu, moved)) {
+    if (__any_sync(0xFFFFFFFFu, over)) {
+      top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      top = max(top & 0xFFFFu, top >> 16);
+      lift = min(lift, 29 - kHead - (int)(top >> 10));  // top < 2^(exponent - 14): weight * scale < 2^15
+      cap = ((uint32_t)(30 - kHead - lift) << 10) - 1u;
+      cap |= cap << 16;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        l[t] *= corr[t];
-        const float c0 = __shfl_sync(0xFFFFFFFFu, corr[t], 8 * tig), c1 = __shfl_sync(0xFFFFFFFFu, corr[t], 8 * tig + 4);
+        mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xFFFFFFFFu, mx[t], 1));
+        mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xFFFFFFFFu, mx[t], 2));
+        const bool first = m[t] == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
+        m[t] = fmaxf(m[t], mx[t]);
+        const float r = (m[t] == -INFINITY ? 0.f : m[t]) - (float)lift, corr = first ? 0.f : ex2(ref[t] - r);
+        ref[t] = r;
+        const float c0 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig), c1 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) oz[t][i] *= (i & 1) ? c1 : c0;
 #pragma unroll
@@ -391,21 +429,21 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
     // weights and values
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      const uint32_t tile = smem_u32(tiles + u * L::kBytes);
+      const uint8_t* tile = tiles + u * L::kBytes;
       uint32_t vs[2 * G], vz[2];
 #pragma unroll
       for (int v = 0; v < 2 * G / 4; ++v) {
-        const uint4 y = lds128(tile + L::kVs + v * 64 + tig * 16);
+        const uint4 y = lds_u4(tile + L::kVs + v * 64 + tig * 16);
         vs[4 * v] = y.x; vs[4 * v + 1] = y.y; vs[4 * v + 2] = y.z; vs[4 * v + 3] = y.w;
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        vz[n] = gid < G ? lds32(tile + L::kVz + gid * 32 + n * 16 + tig * 4) : 0u;
+        vz[n] = gid < G ? lds_u1(tile + L::kVz + gid * 32 + n * 16 + tig * 4) : gid == G ? 0x3C003C00u : 0u;
         if constexpr (kMasked) {
           const int p = pos + 16 * u + 8 * n + 2 * tig;
           vz[n] = finite2(vz[n]);
-          if (p >= p1) vz[n] &= 0xFFFF0000u;
-          if (p + 1 >= p1) vz[n] &= 0xFFFFu;
+          if (p >= p1 && gid < G) vz[n] &= 0xFFFF0000u;
+          if (p + 1 >= p1 && gid < G) vz[n] &= 0xFFFFu;
         }
       }
       uint32_t wp[NT][2], wl[NT][2];  // weights of positions 2 tig, 2 tig + 1 (+ 8); low parts
@@ -413,22 +451,24 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[t][i] = ex2(s[t][u][i] - ref[t]);
-          l[t] += w[t][i];
+        for (int i = 0; i < 4; i += 2) {
+          const float2 e = __ffma2_rn(make_float2(s[t][u][i], s[t][u][i + 1]), make_float2(kscale[t], kscale[t]),
+                                      make_float2(-ref[t], -ref[t]));
+          w[t][i] = ex2(e.x);
+          w[t][i + 1] = ex2(e.y);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           if constexpr (kF32) split2(w[t][2 * n], w[t][2 * n + 1], wp[t][n], wl[t][n]);
           else wp[t][n] = pack_h(w[t][2 * n], w[t][2 * n + 1]);
         }
-        mma16816(oz[t], vz[0], 0u, vz[1], 0u, wp[t][0], wp[t][1]);
-        if constexpr (kF32) mma16816(oz[t], vz[0], 0u, vz[1], 0u, wl[t][0], wl[t][1]);
+        mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);  // (rows 8..15 are not used)
+        if constexpr (kF32) mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wl[t][0], wl[t][1]);
       }
       uint32_t vc[2 * G];
 #pragma unroll
       for (int v = 0; v < 2 * G / 4; ++v) {
-        const uint4 x = lds128(tile + L::kV + v * 512 + lane * 16);
+        const uint4 x = lds_u4(tile + L::kV + v * 512 + lane * 16);
         vc[4 * v] = x.x; vc[4 * v + 1] = x.y; vc[4 * v + 2] = x.z; vc[4 * v + 3] = x.w;
       }
 #pragma unroll
@@ -490,11 +530,10 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   float* ml = ob + kWarps * kRows * D;                   // [warp][row][2]
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 1);
-    l[t] += __shfl_xor_sync(0xFFFFFFFFu, l[t], 2);
-    if (tig == 0) {
-      ml[(warp * kRows + 8 * t + gid) * 2] = m[t] == -INFINITY && l[t] == 0.f ? -INFINITY : ref[t];
-      ml[(warp * kRows + 8 * t + gid) * 2 + 1] = l[t];
+    if (tig == 0) ml[(warp * kRows + 8 * t + gid) * 2] = ref[t];
+    if (gid == G) {  // the row of ones has the sums of the weights
+      ml[(warp * kRows + 8 * t + 2 * tig) * 2 + 1] = oz[t][0];
+      ml[(warp * kRows + 8 * t + 2 * tig + 1) * 2 + 1] = oz[t][1];
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -516,11 +555,12 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
     if (row > last_row) break;
     float top = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * kRows + r) * 2]);
+    for (int w = 0; w < kWarps; ++w)  // a sum of zero: this warp had nothing for the row
+      top = fmaxf(top, ml[(w * kRows + r) * 2 + 1] == 0.f ? -INFINITY : ml[(w * kRows + r) * 2]);
     float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = top == -INFINITY ? 0.f : ex2(ml[(w * kRows + r) * 2] - top);
+      const float f = ml[(w * kRows + r) * 2 + 1] == 0.f ? 0.f : ex2(ml[(w * kRows + r) * 2] - top);
       sum = fmaf(f, ml[(w * kRows + r) * 2 + 1], sum);
       const float* src = ob + (w * kRows + r) * D + 8 * w8;
 #pragma unroll
@@ -539,41 +579,63 @@ __global__ void __launch_bounds__(kThreadsA) attn_few(const AttnArgs a) {
   }
 }
 
-// Joins the splits of a row: grid (sequence, kv head, row tile), D / 8 threads a row.
+// Joins the splits of a row, a CTA per row: a warp's lanes look at the splits' references
+// and sums together, then D / 4 threads per split sum the values, all loads independent.
 template <int D, class T, int NT>
 __global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
-  constexpr int kRows = 8 * NT;
-  int idx = blockIdx.x;
+  constexpr int kRows = 8 * NT, kPer = D / 4, kGroups = 128 / kPer;
+  __shared__ float4 red[kGroups][kPer];
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x % kRows, tile = blockIdx.x / kRows;
+  int idx = tile;
   const int rt = a.n_rt - 1 - idx % a.n_rt;
   idx /= a.n_rt;
   const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
   const Kv4Seq seq = kv4_seq(a.b, si);
-  if (!seq.ok) return;
-  const int n_rows = seq.n * a.rep, row0 = rt * kRows, last_row = min(n_rows, row0 + kRows) - 1;
+  const int n_rows = seq.n * a.rep, row0 = rt * kRows, last_row = min(n_rows, row0 + kRows) - 1, row = row0 + r;
   const int see_any = max(0, seq.len - seq.n + last_row / a.rep + 1);
   const int n = max(1, min(a.n_split, (see_any + a.split_len - 1) / a.split_len));
-  for (int e = threadIdx.x; e < kRows * (D / 8); e += 128) {
-    const int r = e / (D / 8), w8 = e % (D / 8), row = row0 + r;
-    if (row > last_row) break;
-    const float* part = a.part + ((size_t)blockIdx.x * a.n_split * kRows + r) * (D + 4);
-    const size_t stride = (size_t)kRows * (D + 4);
-    float top = -INFINITY;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, part[s * stride]);
-    float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < n; ++s) {
-      const float* p = part + s * stride;
-      const float f = top == -INFINITY ? 0.f : ex2(p[0] - top);
-      sum = fmaf(f, p[1], sum);
-      float y[8];
-      load8<float>(p + 4 + 8 * w8, y);
+  const float* part = a.part + ((size_t)tile * a.n_split * kRows + r) * (D + 4);
+  const size_t stride = (size_t)kRows * (D + 4);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the splits' kernel is done and its writes are seen
+  if (!seq.ok || row > last_row) return;
+  float top = -INFINITY;
+  for (int s = lane; s < n; s += 32) top = fmaxf(top, __ldcg(part + s * stride));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fmaf(f, y[i], x[i]);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv;
-    store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const int g = threadIdx.x / kPer, w = threadIdx.x % kPer;
+  float sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = g; s < n; s += kGroups) {
+    const float* p = part + s * stride;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 4 + 4 * w));
+    const float f = top == -INFINITY ? 0.f : ex2(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+    x.x = fmaf(f, y.x, x.x);
+    x.y = fmaf(f, y.y, x.y);
+    x.z = fmaf(f, y.z, x.z);
+    x.w = fmaf(f, y.w, x.w);
   }
+  __shared__ float sums[kGroups];
+  red[g][w] = x;
+  if (w == 0) sums[g] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D / 8) return;
+  float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float4 u = red[i][2 * threadIdx.x], v = red[i][2 * threadIdx.x + 1];
+    y[0] += u.x; y[1] += u.y; y[2] += u.z; y[3] += u.w;
+    y[4] += v.x; y[5] += v.y; y[6] += v.z; y[7] += v.w;
+    sum += sums[i];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] *= inv;
+  store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * threadIdx.x * sizeof(T), y);
 }
 
 struct Plan {
@@ -595,18 +657,21 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   const long long base = (long long)b->n_seqs * c->n_kv_heads * n_rt;
   const int unit = MK_KV4_PAGE;
   const long long pages = (b->max_len + unit - 1) / unit;
+  // Splits: enough that every SM has about two CTAs, in pieces of at least a page per warp
+  // (one sequence of 8200 positions, 8 kv heads of 64: 15.9 us with 4 splits, 9.1 with 32);
+  // and where there are more, up to eight CTAs per SM in pieces of 32 pages, so that
+  // sequences of unequal length fill the SMs evenly (64 of up to 16384 positions, kv heads
+  // of 128: 190 us unsplit, 146 so; 64 of about 2000 lose by a split, 55 to 65 us).
   long long n_split = 1;
-  if (base > 0 && pages > kWarps) {
-    const long long want = (6ll * sms + base - 1) / base;  // about six CTAs per SM
-    n_split = std::max(1ll, std::min(want, pages / kWarps));
-  }
+  if (base > 0)
+    n_split = std::max({1ll, std::min(2ll * sms / base, pages / kWarps), std::min(8ll * sms / base, pages / 32)});
   const long long per = std::max(1ll, (pages + n_split - 1) / n_split);
   n_split = std::max(1ll, (pages + per - 1) / per);
   p->n_rt = (int)n_rt;
   p->n_split = (int)n_split;
   p->split_len = (int)std::min<long long>(per * unit, 0x7FFFFFC0);
   p->ctas = base * n_split;
-  if (p->ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
+  if (p->ctas > 0x7FFFFFFF / 64) return MK_ERR_UNSUPPORTED;
   p->part_bytes = n_split > 1 ? p->ctas * 8 * p->nt * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
   return MK_OK;
 }
@@ -629,7 +694,19 @@ mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT>), kSmem, &ready)) return MK_ERR_CUDA;
   attn_few<D, T, NT><<<(unsigned)p.ctas, kThreadsA, kSmem, s>>>(a);
-  if (p.n_split > 1) attn_join<D, T, NT><<<(unsigned)(p.ctas / p.n_split), 128, 0, s>>>(a);
+  if (p.n_split > 1) {
+    // launched while the splits run (its first loads wait for them)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.ctas / p.n_split * 8 * NT));
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, attn_join<D, T, NT>, a) != cudaSuccess) return MK_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

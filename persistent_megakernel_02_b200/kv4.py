@@ -15,23 +15,16 @@ from __future__ import annotations
 import ctypes
 import math
 
+import torch
+
 from . import MkError, MkKv4Batch, MkKv4CacheStruct, MkKv4Rows, _check, lib
 
 PAGE = 64
-_DTYPES = None
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
 def _bad(what, why):
     raise MkError(1, f"{what}: {why}")
-
-
-def _dtype_code(dtype):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-
-        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    return _DTYPES.get(dtype)
 
 
 def page_bytes(head_dim: int) -> int:
@@ -48,8 +41,6 @@ class Kv4Batch:
     :meth:`Kv4Cache.batch`)."""
 
     def __init__(self, cache, block_table, cu, kv_lens, n_rows, max_new, max_len):
-        import torch
-
         for name, t, dims in (("block_table", block_table, 2), ("cu", cu, 1), ("kv_lens", kv_lens, 1)):
             if t is None or t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
                 _bad("Kv4Batch", f"{name} must be a contiguous int32 tensor with {dims} dimension(s)")
@@ -68,7 +59,6 @@ class Kv4Batch:
         self._workspace_bytes = {}
         self._struct = MkKv4Batch(block_table.data_ptr(), cu.data_ptr(), kv_lens.data_ptr(), n, max_pages,
                                   int(n_rows), min(int(max_new), int(n_rows)), int(max_len))
-        self._ref = ctypes.byref(self._struct)
 
 
 class Kv4Cache:
@@ -81,8 +71,6 @@ class Kv4Cache:
     """
 
     def __init__(self, pool, block_table=None, head_dim: int = 128):
-        import torch
-
         if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous() or not pool.is_cuda:
             _bad("Kv4Cache", "pool must be a contiguous uint8 CUDA tensor [n_layers, n_pages, n_kv_heads, page_bytes]")
         if int(pool.shape[3]) != page_bytes(head_dim) or pool.numel() == 0:
@@ -93,13 +81,14 @@ class Kv4Cache:
         self._status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._struct = MkKv4CacheStruct(pool.data_ptr(), self._status.data_ptr(), self.n_layers, self.n_pages,
                                         self.n_kv_heads, self.head_dim)
-        self._ref = ctypes.byref(self._struct)
+        self._index = pool.device.index
+        self._scale = 1.0 / math.sqrt(head_dim)
+        so = lib()
+        self._append, self._read, self._attention = so.mk_kv4_append, so.mk_kv4_read, so.mk_kv4_attention
 
     @classmethod
     def empty(cls, n_layers, n_pages, n_kv_heads, head_dim, block_table=None, device="cuda"):
         """A cache with a pool of its own."""
-        import torch
-
         pool = torch.empty((n_layers, n_pages, n_kv_heads, page_bytes(head_dim)), dtype=torch.uint8, device=device)
         return cls(pool, block_table, head_dim)
 
@@ -112,40 +101,40 @@ class Kv4Cache:
                         max_new, max_len)
 
     def _launch(self, what, stream):
-        import torch
-
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             _bad(what, f"the cache is not on the current CUDA device ({torch.cuda.current_device()})")
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            return torch.cuda.current_stream(self._index).cuda_stream
         return getattr(stream, "cuda_stream", stream)
 
-    def _rows(self, what, name, t, heads, batch, code):
-        if t.dim() != 3 or tuple(t.shape) != (batch.n_rows, heads, self.head_dim):
+    def _rows(self, what, name, t, heads, batch, dtype):
+        if t.shape != (batch.n_rows, heads, self.head_dim):
             _bad(what, f"{name} must have shape ({batch.n_rows}, {heads}, {self.head_dim}), got {tuple(t.shape)}")
-        if t.device != self.device:
+        if t.dtype is not dtype or dtype not in _DTYPES:
+            _bad(what, f"{name} must be bfloat16, float16 or float32, the same type for every tensor; got {t.dtype}")
+        if t.get_device() != self._index:
             _bad(what, f"{name} must be on {self.device}")
         rs, hs, es = t.stride()
         if es != 1:
             _bad(what, f"the last dimension of {name} must be contiguous")
-        if _dtype_code(t.dtype) != code or code is None:
-            _bad(what, f"{name} must be bfloat16, float16 or float32, the same type for every tensor; got {t.dtype}")
         return MkKv4Rows(t.data_ptr(), rs, hs)
 
     def _kv(self, fn, what, layer, k, v, batch, stream):
-        code = _dtype_code(k.dtype)
-        kr = self._rows(what, "k", k, self.n_kv_heads, batch, code)
-        vr = self._rows(what, "v", v, self.n_kv_heads, batch, code)
-        _check(fn(self._ref, layer, batch._ref, kr, vr, code, self._launch(what, stream)), what)
+        dtype = k.dtype
+        kr = self._rows(what, "k", k, self.n_kv_heads, batch, dtype)
+        vr = self._rows(what, "v", v, self.n_kv_heads, batch, dtype)
+        st = fn(self._struct, layer, batch._struct, kr, vr, _DTYPES[dtype], self._launch(what, stream))
+        if st:
+            raise MkError(st, what)
 
     def append(self, layer, k, v, batch, stream=None):
         """Quantise rows ``k`` and ``v`` ([n_rows, n_kv_heads, head_dim], any row and head
         strides) into their positions."""
-        self._kv(lib().mk_kv4_append, "mk_kv4_append", layer, k, v, batch, stream)
+        self._kv(self._append, "mk_kv4_append", layer, k, v, batch, stream)
 
     def read(self, layer, k, v, batch, stream=None):
         """Write the values the cache holds for the batch's rows into ``k`` and ``v``."""
-        self._kv(lib().mk_kv4_read, "mk_kv4_read", layer, k, v, batch, stream)
+        self._kv(self._read, "mk_kv4_read", layer, k, v, batch, stream)
 
     def attend(self, layer, q, out, batch, scale=None, workspace=None, stream=None):
         """Causal attention of query rows ``q`` [n_rows, n_heads, head_dim] over the cache,
@@ -153,16 +142,16 @@ class Kv4Cache:
         1 / sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of ``workspace_bytes`` for calls
         that must not allocate; otherwise one is allocated on the launch stream."""
         what = "mk_kv4_attention"
-        heads = int(q.shape[1]) if q.dim() == 3 else 0
-        code = _dtype_code(q.dtype)
-        qr = self._rows(what, "q", q, heads, batch, code)
-        orow = self._rows(what, "out", out, heads, batch, code)
+        dtype = q.dtype
+        heads = q.shape[1] if q.dim() == 3 else 0
+        qr = self._rows(what, "q", q, heads, batch, dtype)
+        orow = self._rows(what, "out", out, heads, batch, dtype)
         raw = self._launch(what, stream)
-        need = self.workspace_bytes(batch, heads, q.dtype)
+        need = batch._workspace_bytes.get((heads, dtype))
+        if need is None:
+            need = self.workspace_bytes(batch, heads, dtype)
         ptr = None
         if need:
-            import torch
-
             if workspace is None:
                 if stream is None:
                     workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
@@ -170,20 +159,20 @@ class Kv4Cache:
                     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, self.device)
                     with torch.cuda.stream(s):
                         workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-            elif workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous():
+            elif workspace.dtype != torch.uint8 or workspace.get_device() != self._index or not workspace.is_contiguous():
                 _bad(what, f"workspace must be a contiguous uint8 tensor on {self.device}")
             need, ptr = workspace.numel(), workspace.data_ptr()
-        _check(lib().mk_kv4_attention(self._ref, layer, batch._ref, qr, orow, heads, code,
-                                      1.0 / math.sqrt(self.head_dim) if scale is None else scale,
-                                      ptr, need, raw), what)
+        st = self._attention(self._struct, layer, batch._struct, qr, orow, heads, _DTYPES[dtype],
+                             self._scale if scale is None else scale, ptr, need, raw)
+        if st:
+            raise MkError(st, what)
 
     def workspace_bytes(self, batch, n_heads, dtype) -> int:
         """Workspace of :meth:`attend` for this batch (0 where it needs none)."""
         got = batch._workspace_bytes.get((n_heads, dtype))
         if got is None:
             n = ctypes.c_int64()
-            code = _dtype_code(dtype)
-            _check(lib().mk_kv4_attention_workspace(self._ref, batch._ref, n_heads, -1 if code is None else code,
+            _check(lib().mk_kv4_attention_workspace(self._struct, batch._struct, n_heads, _DTYPES.get(dtype, -1),
                                                     ctypes.byref(n)), "mk_kv4_attention_workspace")
             got = batch._workspace_bytes[(n_heads, dtype)] = n.value
         return got
@@ -191,8 +180,6 @@ class Kv4Cache:
     def check(self, stream=None):
         """Wait for ``stream`` and raise MkError if a call met numbers outside its batch's
         bounds or a page id outside the pool since the last check."""
-        import torch
-
         raw = self._launch("Kv4Cache.check", stream)
         with torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device)):
             bits = int(self._status.item())
