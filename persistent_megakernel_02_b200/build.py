@@ -29,6 +29,7 @@ UNITS = [
     ("mk_prefill", "mk_prefill.cu", []),
     ("mk_kv4", "mk_kv4.cu", []),
     ("mk_kv4_attn", "mk_kv4_attn.cu", []),
+    ("mk_kv4_prompt", "mk_kv4_prompt.cu", []),
 ] + [(f"mk_inst_s{s}_n{n}", "mk_inst.cu", [f"-DMK_SPEC={s}", f"-DMK_NBT={n}"])
      for s in (0, 1, 2) for n in (8, 4, 2, 1)]
 DEPS = ["mk_kernel.cuh", "mk_device.cuh", "mk_matvec.cuh", "mk_plan.h", "mk_tc.cuh", "mk_kv4.cuh", "mk_kv4.h"]

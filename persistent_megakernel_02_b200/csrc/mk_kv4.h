@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/mk.h"
 
 namespace mk {
@@ -12,6 +14,23 @@ mk_status kv4_check_cache(const mk_kv4_cache* c);
 mk_status kv4_check(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, int32_t dtype);
 // `written`: the rows are an output, so they must not overlap
 mk_status kv4_check_rows(const mk_kv4_rows* r, int32_t dtype, int64_t rows, int32_t heads, int32_t d, bool written);
+
+// The arguments every attention kernel takes.
+struct Kv4Attn {
+  mk_kv4_cache c;
+  mk_kv4_batch b;
+  const char* q;
+  char* out;
+  long long q_row, q_head, o_row, o_head;  // strides in bytes
+  int layer, rep;
+  float scale_log2;  // scale * log2(e)
+};
+
+// Opt-in to more than 48 KiB of shared memory, once per kernel and device.
+bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready);
+
+// Attention of many query rows of 16-bit types (mk_kv4_prompt.cu).
+mk_status kv4_prompt(const Kv4Attn& a, int32_t dtype, cudaStream_t s);
 
 // Quantise (write) or read back positions start .. start + n - 1 of a slot of a handle's
 // cache [layer][physical page][kv head][K, V][PL][d], all layers; arguments checked by the caller.

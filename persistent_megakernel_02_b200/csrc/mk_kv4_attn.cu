@@ -39,17 +39,10 @@ constexpr int kStages = 2;  // ring depth per warp
 constexpr int kHead = 4;    // log2 of what a weight may pass the reference by
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
-struct AttnArgs {
-  mk_kv4_cache c;
-  mk_kv4_batch b;
-  const char* q;
-  char* out;
-  long long q_row, q_head, o_row, o_head;  // strides in bytes
-  int layer, rep;
-  float scale_log2;  // scale * log2(e)
+struct AttnArgs : Kv4Attn {
   int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page)
   int n_rt;                // row tiles
-  float* part;             // [seq][kv head][row tile][split][8 NT][D + 2]
+  float* part;             // [seq][kv head][row tile][split][8 NT][D + 4]
 };
 
 // c += A B (16 x 16 by 16 x 8), and the same from zero
@@ -639,6 +632,7 @@ __global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
 }
 
 struct Plan {
+  bool prompt;  // many rows of 16-bit queries: the tcgen05 kernel, unsplit
   int nt, n_rt, n_split, split_len;
   long long ctas;
   int64_t part_bytes;
@@ -651,6 +645,12 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MK_ERR_CUDA;
   const long long rows = std::max<long long>(b->max_new, 1) * rep;  // 0: still looks at the spans
+  p->prompt = dtype != 2 && rows >= 128;
+  if (p->prompt) {
+    p->n_split = 1;
+    p->part_bytes = 0;
+    return MK_OK;
+  }
   const int most = c->head_dim == 64 && dtype != 2 ? 4 : 2;
   p->nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
   const long long n_rt = (rows + 8 * p->nt - 1) / (8 * p->nt);
@@ -674,17 +674,6 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   if (p->ctas > 0x7FFFFFFF / 64) return MK_ERR_UNSUPPORTED;
   p->part_bytes = n_split > 1 ? p->ctas * 8 * p->nt * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
   return MK_OK;
-}
-
-// Opt-in to more than 48 KiB of shared memory, once per kernel and device.
-bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (ready->load(std::memory_order_relaxed) & bit) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  ready->fetch_or(bit, std::memory_order_relaxed);
-  return true;
 }
 
 template <int D, class T, int NT>
@@ -728,6 +717,17 @@ mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_bat
 }
 
 }  // namespace
+
+bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready->load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  ready->fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 }  // namespace mk
 
 using namespace mk;
@@ -762,11 +762,12 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
   if (p.part_bytes > 0 && (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < p.part_bytes))
     return MK_ERR_INVALID_ARG;
   const int size = dtype == 2 ? 4 : 2;
-  const AttnArgs a{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p),
-                   q->row_stride * size, q->head_stride * size, out->row_stride * size, out->head_stride * size,
-                   layer, rep, scale * 1.44269504088896341f, p.n_split, p.split_len, p.n_rt,
-                   static_cast<float*>(workspace)};
+  AttnArgs a{{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p), q->row_stride * size,
+              q->head_stride * size, out->row_stride * size, out->head_stride * size, layer, rep,
+              scale * 1.44269504088896341f},
+             p.n_split, p.split_len, p.n_rt, static_cast<float*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.prompt) return kv4_prompt(a, dtype, s);
   if (cache->head_dim == 64) {
     if (dtype == 0) return launch_few<64, __nv_bfloat16>(a, p, s);
     if (dtype == 1) return launch_few<64, __half>(a, p, s);
