@@ -86,6 +86,27 @@ __device__ __forceinline__ uint8_t* kv4_tile(const mk_kv4_cache& c, const int32_
   return static_cast<uint8_t*>(c.pool) + at * Kv4<D>::kBytes;
 }
 
+// Waits for a phase of an mbarrier, a bounded number of tries; on expiry the cache's
+// status word says so.  A look first (27 cycles where the phase is over, the suspending
+// try takes 100), then tries that may suspend the thread for 10 us (spinning instead takes
+// issue slots from the other warps: a 2048-token prompt 79 -> 82 us).
+constexpr int kKv4Tries = 1 << 20;
+__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  uint32_t over;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(over)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (over) return true;
+  for (int i = 0; i < kKv4Tries; ++i)
+    if (mbar_try_wait_hint(bar, parity, 10000)) return true;
+  atomicOr(status, KV4_TIMEOUT);
+  return false;
+}
+
 // ---- rows of 16-bit or 32-bit values ----
 template <class T>
 struct Raw8 {  // 8 values as they are in memory

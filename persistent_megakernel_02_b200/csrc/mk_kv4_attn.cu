@@ -37,7 +37,6 @@ constexpr int kThreadsA = 32 * kWarps;
 constexpr int kStageBytes = 5120;
 constexpr int kStages = 2;  // ring depth per warp
 constexpr int kHead = 4;    // log2 of what a weight may pass the reference by
-constexpr unsigned long long kWaitNs = 1000000000ull;
 
 struct AttnArgs : Kv4Attn {
   int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page)
@@ -84,19 +83,6 @@ __device__ __forceinline__ uint32_t finite2(uint32_t a) {
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_h(x, y);
   lo = pack_h(x - h_lo(hi), y - h_hi(hi));
-}
-
-// Waits for a phase with a limit; on expiry the cache's status word says so.
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_hint(bar, parity, 1000)) {
-    if (globaltimer_ns() - t0 > kWaitNs) {
-      atomicOr(status, KV4_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
 }
 
 // One CTA: the rows of a row tile (8 NT rows: query tokens x the rep heads of one kv
@@ -498,7 +484,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   bool alive = true;
   for (int i = 0; i < mine; ++i) {
     const int slot = i % kStages, s = s0 + warp + kWarps * i;
-    alive = __all_sync(0xFFFFFFFFu, wait_full(&full[warp][slot], (i / kStages) & 1, a.c.status));
+    alive = __all_sync(0xFFFFFFFFu, kv4_wait(&full[warp][slot], (i / kStages) & 1, a.c.status));
     if (!alive) break;
     if (!slot_bad[warp][slot]) {
       const uint8_t* tiles = ring + slot * kStageBytes;
@@ -514,7 +500,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     if (i + kStages < mine) issue(i + kStages);
   }
   if (!alive) {  // copies still in flight must land before the CTA's shared memory goes
-    for (int i = 0; i < kStages; ++i) wait_full(&full[warp][i], 0, a.c.status), wait_full(&full[warp][i], 1, a.c.status);
+    for (int i = 0; i < kStages; ++i) kv4_wait(&full[warp][i], 0, a.c.status), kv4_wait(&full[warp][i], 1, a.c.status);
   }
 
   // ---- merge of the warps' states, in the ring's memory ----

@@ -5,7 +5,7 @@
 // 128, and walks the positions it sees in tiles of 128.  Roles:
 //   warps 0-3, 4-7  softmax of query tile 0, 1: one thread per row
 //   warps 8-11      dequantise: codes to fp16 K and V in the swizzled shared-memory layout
-//   warp 12         issues the matrix instructions
+//   warps 12, 13    issue the matrix instructions of query tile 0, 1
 // Per tile: S = Q K^T into tensor memory (128 x 128 fp32); the row's thread reads S twice
 // (maximum, then weights) and writes the weights back over S as fp16, from where they are
 // the A operand of O += W V, which stays in tensor memory.  The two query tiles alternate:
@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mk_kv4.cuh"
 #include "mk_kv4.h"
@@ -30,11 +31,10 @@
 namespace mk {
 namespace {
 
-constexpr int kPThreads = 13 * 32;
+constexpr int kPThreads = 14 * 32;
 constexpr int kPTile = 128;  // positions per tile, and rows per query tile
 constexpr int kPHead = 4;    // log2 of what a weight may pass the reference by
 constexpr int kPLift = 10;   // weights are 2^(score - m + kPLift), at most 2^14
-constexpr unsigned long long kPWaitNs = 1000000000ull;
 
 template <int D>
 struct PSmem {
@@ -44,27 +44,49 @@ struct PSmem {
 };
 
 struct PShared {
-  uint64_t q_full, kv_full[2], kv_empty[2], s_full[2], w_full[2], o_full[2], drained;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], w_full[2][2], wv_done[2], o_full[2], drained[2];
   uint32_t tmem;
-  // what a tile needs special care for: bits 0-3 blocks of 32 positions whose page is
-  // out of range, bit 4 + w block w holds NaN values
-  uint32_t special[2][4];
-  uint8_t nan_groups[2][kPTile];  // groups of V that are NaN, by position (valid where bit 4 + w is set)
+  uint32_t bad[2][4];  // blocks of 32 positions whose page id is out of range
+  // first position whose V is NaN, by group: it is zero in the product (0 x NaN would reach
+  // rows that do not see it) and put into the rows that see it at the end
+  int nan_first[4];
 };
 
 // instruction descriptor: D fp32, A and B fp16, both K-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[bdesc]^T: A's rows are tensor-memory lanes, two fp16 per column
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t acc) {
-  const uint32_t z = 0;
+// The issuing warp stays converged and one lane's predicate is inside the statement, so
+// that descriptors live in uniform registers (from a branch of one lane each instruction
+// took about 80 cycles to issue).
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(z), "r"(z), "r"(z), "r"(z));
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one));
+}
+// A in tensor memory: its rows are the lanes, two fp16 values per column
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one));
+}
+__device__ __forceinline__ void mma_commit(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+  return e;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -84,15 +106,21 @@ __device__ __forceinline__ void tmem_get16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_get32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_get64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, "
+      "%23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, "
+      "%44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
@@ -102,6 +130,11 @@ __device__ __forceinline__ float pex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // at the rate of a maximum of two
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
@@ -127,18 +160,6 @@ __device__ __forceinline__ uint32_t both(uint32_t pair, int which) {  // one hal
 }
 __device__ __forceinline__ bool nan_half(uint32_t h) { return (h & 0x7FFFu) > 0x7C00u; }
 
-__device__ __forceinline__ bool pwait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait_hint(bar, parity, 1000)) {
-    if (globaltimer_ns() - t0 > kPWaitNs) {
-      atomicOr(status, KV4_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-
 // 16-byte chunk c (0..7) of row r in a tile of 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
@@ -152,7 +173,7 @@ template <int D, class T>
 __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int n_blocks) {
   using L = Kv4<D>;
   constexpr int G = L::G;
-  constexpr uint32_t kIdQK = idesc_f16(128, kPTile), kIdWV = idesc_f16(128, D);
+  constexpr uint32_t kIdQK = idesc_f16(128, 64), kIdWV = idesc_f16(128, D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ PShared sh;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -172,23 +193,29 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
   const int n_rows = seq.n * a.rep, row0 = blk * 2 * kPTile;
   if (row0 >= n_rows) return;
   const int start = seq.len - seq.n;  // position of the first query token (may be negative)
-  int n_tiles[2], n_max = 0;          // tiles of positions each query tile sees
+  int n_half[2], n_max = 0;           // halves of 64 positions each query tile sees; tiles of 128
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int first = row0 + t * kPTile, last = min(n_rows, first + kPTile) - 1;
-    n_tiles[t] = first < n_rows ? (max(0, start + last / a.rep + 1) + kPTile - 1) / kPTile : 0;
-    n_max = max(n_max, n_tiles[t]);
+    n_half[t] = first < n_rows ? (max(0, start + last / a.rep + 1) + 63) / 64 : 0;
+    n_max = max(n_max, (n_half[t] + 1) / 2);
   }
 
+  if (tid < 4) sh.nan_first[tid] = 0x7FFFFFFF;
   if (tid == 0) {
     mbar_init(&sh.q_full, 2 * kPTile);
-    mbar_init(&sh.drained, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.kv_full[i], kPTile);
-      mbar_init(&sh.kv_empty[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.w_full[i], kPTile);
+      mbar_init(&sh.k_full[i], kPTile);
+      mbar_init(&sh.k_empty[i], 2);
+      mbar_init(&sh.v_full[i], kPTile);
+      mbar_init(&sh.v_empty[i], 2);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh.s_full[i][h], 1);
+        mbar_init(&sh.w_full[i][h], 4);
+      }
+      mbar_init(&sh.wv_done[i], 1);
       mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.drained[i], 1);
     }
     fence_barrier_init();
   }
@@ -196,7 +223,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;  // S0, S1: 128 columns each; O0, O1: D each
+  // Columns: S0, S1 128 each (two halves of 64 positions), O0, O1 D each.  The weights of a
+  // half, 32 columns, lie over the scores of that half.
+  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t kO = 256;
 
   if (warp < 8) {
     // ---------------- softmax: one thread per row ----------------
@@ -204,14 +234,17 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     const bool live = row < n_rows;
     float kscale;
     {
-      float mx = 0.f;
       const char* src = a.q + (long long)(seq.row0 + row / a.rep) * a.q_row +
                         (long long)(head * a.rep + row % a.rep) * a.q_head;
       Raw8<T> raw[D / 8];
+      float mx = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         raw[c] = Raw8<T>{};
         if (live) raw[c] = load_raw8<T>(src + c * 16);
+      }
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
         float x[8];
         unpack8(raw[c], x);
 #pragma unroll
@@ -240,92 +273,79 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     const int lim_warp = start + (row0 + t * kPTile + (r_in & ~31)) / a.rep + 1;  // the warp's rows all see these
     const bool whole = row0 + t * kPTile + (r_in | 31) < n_rows;      // no row of the warp is past the end
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t ts = lane_base + (uint32_t)(t * 128), to = lane_base + (uint32_t)(256 + t * D);
+    const uint32_t ts = lane_base + (uint32_t)(t * 128), to = lane_base + kO + (uint32_t)(t * D);
     float m = -INFINITY, ref = 0.f, sum = 0.f;
-    uint32_t nan_out = 0;  // groups of the output that a NaN value reaches
-    const int n = n_tiles[t];
+    const int n = n_half[t];
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = __all_sync(0xFFFFFFFFu, pwait(&sh.s_full[t], j & 1, a.c.status));
+    for (int i = 0; i < n; ++i) {
+      const int h = i & 1, buf = (i >> 1) & 1;
+      ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.s_full[t][h], buf, a.c.status));
       if (!ok) break;
       tc_fence_after();
-      const int base = j * kPTile, left = lim - base;  // columns with position < left are seen
-      uint32_t special = 0;
+      uint32_t s[64];
+      tmem_get64(ts + 64 * h, s);
+      const int base = i * 64, left = lim - base;  // columns with position < left are seen
+      const uint32_t bad0 = sh.bad[buf][2 * h], bad1 = sh.bad[buf][2 * h + 1];
+      float mx;
+      if (whole && base + 64 <= lim_warp && (bad0 | bad1) == 0) {
+        float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) special |= sh.special[j & 1][w];
-      const bool plain = whole && base + kPTile <= lim_warp && special == 0;
-      auto masked = [&](int c) {  // column c
-        return column_position(c) >= left || (special >> (c >> 5) & 1u);
-      };
-      // maximum
-      float mx = -INFINITY;
+        for (int c = 0; c < 64; c += 2)
+          q[(c >> 1) & 3] = max3(q[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        mx = fmaxf(max3(q[0], q[1], q[2]), q[3]) * kscale;
+      } else {  // (with a maximum of its own: a mask in the common code is paid by every tile)
+        mx = -INFINITY;
 #pragma unroll
-      for (int c0 = 0; c0 < kPTile; c0 += 32) {
-        uint32_t s[32];
-        tmem_get32(ts + c0, s);
-        if (plain) {
-          float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            q[(i >> 1) & 3] = fmaxf(q[(i >> 1) & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-          mx = fmaxf(mx, fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = masked(c0 + i) ? mx : fmaxf(mx, __uint_as_float(s[i]));
+        for (int c = 0; c < 64; ++c) {
+          if (column_position(c) >= left || (c < 32 ? bad0 : bad1)) s[c] = 0xFF800000u;
+          mx = fmaxf(mx, __uint_as_float(s[c]));
         }
+        mx *= kscale;
       }
-      mx *= kscale;
-      if (__any_sync(0xFFFFFFFFu, mx > m + (float)kPHead)) {
+      if (__any_sync(0xFFFFFFFFu, mx > m + (float)kPHead)) {  // the reference moves: seldom
         const bool first = m == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
         m = fmaxf(m, mx);
         const float r = (m == -INFINITY ? 0.f : m) - (float)kPLift, corr = first ? 0.f : pex2(ref - r);
         ref = r;
         sum *= corr;
-        if (j > 0) {  // O is complete up to the tile before: its product came before this S
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
+        if (i > 0) {  // O, once the product of the half before is in it
+          ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.wv_done[t], (i - 1) & 1, a.c.status));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int d0 = 0; d0 < D; d0 += 16) {
             uint32_t o[16];
-            tmem_get16(to + c0, o);
+            tmem_get16(to + d0, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-            tmem_st16(to + c0, o);
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * corr);
+            tmem_st16(to + d0, o);
           }
         }
       }
-      // weights, over the scores already read
-      float2 part = make_float2(0.f, 0.f);
+      float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       const float2 k2 = make_float2(kscale, kscale), r2 = make_float2(-ref, -ref);
 #pragma unroll
-      for (int c0 = 0; c0 < kPTile; c0 += 32) {
-        uint32_t s[32], w[16];
-        tmem_get32(ts + c0, s);
+      for (int c0 = 0; c0 < 64; c0 += 32) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float2 x = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          if (!plain) {
-            if (masked(c0 + i)) x.x = -INFINITY;
-            if (masked(c0 + i + 1)) x.y = -INFINITY;
-          }
-          x = __ffma2_rn(x, k2, r2);
+        for (int c = 0; c < 32; c += 2) {
+          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), k2, r2);
           x.x = pex2(x.x);
           x.y = pex2(x.y);
-          part = __fadd2_rn(part, x);
-          w[i / 2] = pack_h(x.x, x.y);
+          part[(c >> 1) & 1] = __fadd2_rn(part[(c >> 1) & 1], x);
+          w[c / 2] = pack_h(x.x, x.y);
         }
-        tmem_st16(ts + c0 / 2, w);
+        tmem_st16(ts + 64 * h + c0 / 2, w);  // (over scores that are in registers)
       }
-      sum += part.x + part.y;
-      if (special >> 4) {  // NaN values among this tile's V: zero there, and remembered here
-        for (int c = 0; c < kPTile; ++c) {
-          const int p = column_position(c);
-          if ((sh.special[j & 1][p >> 5] >> (4 + (p >> 5)) & 1u) && !masked(c)) nan_out |= sh.nan_groups[j & 1][p];
-        }
-      }
+      sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sh.w_full[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.w_full[t][h]);
     }
-    if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, pwait(&sh.o_full[t], 0, a.c.status));
+    // (a barrier of its own: the phases of wv_done may be two ahead by now, which a parity
+    // would take for none)
+    if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.o_full[t], 0, a.c.status));
     if (ok) {
       tc_fence_after();
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // 0: the row sees nothing
@@ -334,23 +354,22 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 16) {
         uint32_t o[16];
-        if (n > 0) {
-          tmem_get16(to + c0, o);
-        }
+        if (n > 0) tmem_get16(to + c0, o);
+        const bool nan = n > 0 && sh.nan_first[c0 / 32] < lim;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int hh = 0; hh < 2; ++hh) {
           float x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            x[i] = n > 0 && sum != 0.f ? __uint_as_float(o[8 * h + i]) * inv : 0.f;
-            if (nan_out >> (c0 / 32) & 1u) x[i] = __uint_as_float(0x7FFFFFFFu);
+            x[i] = n > 0 && sum != 0.f ? __uint_as_float(o[8 * hh + i]) * inv : 0.f;
+            if (nan) x[i] = __uint_as_float(0x7FFFFFFFu);
           }
-          if (live) store8<T>(dst + (c0 + 8 * h) * sizeof(T), x);
+          if (live) store8<T>(dst + (c0 + 8 * hh) * sizeof(T), x);
         }
       }
     }
   } else if (warp < 12) {
-    // ---------------- dequantise: warp w has positions 32 w .. 32 w + 31 of a tile ----------------
+    // ---------------- dequantise: warp 8 + w has positions 32 w .. 32 w + 31 of a tile ----------------
     const int w = warp - 8, gid = lane >> 2, tig = lane & 3;
     const int32_t* table = a.b.block_table + (size_t)si * a.b.max_pages;
     const int see = min(seq.len, n_max * kPTile);  // positions behind are left out (zero)
@@ -358,108 +377,65 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     uint4 kc[2][2 * G / 4] = {}, vc[2][2 * G / 4] = {}, vs[2][2 * G / 4] = {}, ks[2][2] = {};
     uint2 kz[2][2] = {};
     uint32_t vz[2][G][2] = {};
-    int page = 0, page_next = 0;
-    auto look = [&](int j) {  // page id of tile j, one tile ahead of its loads
+    // page id of tile j, looked up a tile ahead of its loads; -2: no position there
+    auto look = [&](int j) {
       const int p = j * kPTile + 32 * w;
-      page_next = p < see ? table[p / MK_KV4_PAGE] : -2;  // -2: nothing there
+      return j < n_max && p < see ? table[p / MK_KV4_PAGE] : -2;
     };
-    auto load = [&](int j) {
-      page = page_next;
-      if ((unsigned)page < (unsigned)a.c.n_pages) {
-        const size_t at = (((size_t)a.layer * a.c.n_pages + page) * a.c.n_kv_heads + head) * kKv4Tiles + 2 * (w & 1);
-        const uint8_t* tile = static_cast<const uint8_t*>(a.c.pool) + at * L::kBytes;
+    auto tile_at = [&](int page) {
+      const size_t at = (((size_t)a.layer * a.c.n_pages + page) * a.c.n_kv_heads + head) * kKv4Tiles + 2 * (w & 1);
+      return static_cast<const uint8_t*>(a.c.pool) + at * L::kBytes;
+    };
+    auto load_k = [&](int page) {
+      if ((unsigned)page >= (unsigned)a.c.n_pages) return;
+      const uint8_t* tile = tile_at(page);
 #pragma unroll
-        for (int u = 0; u < 2; ++u, tile += L::kBytes) {
+      for (int u = 0; u < 2; ++u, tile += L::kBytes) {
 #pragma unroll
-          for (int v = 0; v < 2 * G / 4; ++v) {
-            kc[u][v] = ldnc16(tile + v * 512 + lane * 16);
-            vc[u][v] = ldnc16(tile + L::kV + v * 512 + lane * 16);
-            vs[u][v] = ldnc16(tile + L::kVs + v * 64 + tig * 16);
-          }
+        for (int v = 0; v < 2 * G / 4; ++v) kc[u][v] = ldnc16(tile + v * 512 + lane * 16);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            // scales of the groups of rows 2 (gid / 2), + 1 (+ 8 n): a pair per group
-            if constexpr (G == 4) {
-              ks[u][n] = ldnc16(tile + L::kKs + n * 64 + (gid >> 1) * 16);
-              kz[u][n] = __ldg(reinterpret_cast<const uint2*>(tile + L::kKz + (8 * n + gid) * 8));
-            } else {
-              const uint2 s = __ldg(reinterpret_cast<const uint2*>(tile + L::kKs + (gid >> 1) * 16 + n * 8));
-              ks[u][n] = make_uint4(s.x, s.y, 0u, 0u);
-              kz[u][n] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(tile + L::kKz + (8 * n + gid) * 4)), 0u);
-            }
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-              vz[u][g][n] = __ldg(reinterpret_cast<const uint32_t*>(tile + L::kVz + g * 32 + n * 16 + tig * 4));
+        for (int n = 0; n < 2; ++n) {
+          // scales of the groups of rows 2 (gid / 2), + 1 (+ 8 n): a pair per group
+          if constexpr (G == 4) {
+            ks[u][n] = ldnc16(tile + L::kKs + n * 64 + (gid >> 1) * 16);
+            kz[u][n] = __ldg(reinterpret_cast<const uint2*>(tile + L::kKz + (8 * n + gid) * 8));
+          } else {
+            const uint2 s = __ldg(reinterpret_cast<const uint2*>(tile + L::kKs + (gid >> 1) * 16 + n * 8));
+            ks[u][n] = make_uint4(s.x, s.y, 0u, 0u);
+            kz[u][n] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(tile + L::kKz + (8 * n + gid) * 4)), 0u);
           }
         }
-      } else if (page != -2 && lane == 0) {
-        atomicOr(a.c.status, KV4_BAD_PAGE);
       }
-      if (j + 1 < n_max) look(j + 1);
     };
-    look(0);
-    if (n_max > 0) load(0);
-    bool ok = true;
-    for (int j = 0; j < n_max; ++j) {
-      const int buf = j & 1;
-      if (j >= 2) ok = __all_sync(0xFFFFFFFFu, pwait(&sh.kv_empty[buf], ((j >> 1) - 1) & 1, a.c.status));
-      if (!ok) break;
-      uint8_t* sk = skv + buf * 2 * PSmem<D>::kKV;
-      uint8_t* sv = sk + PSmem<D>::kKV;
-      const bool have = (unsigned)page < (unsigned)a.c.n_pages;
-      const int left = have ? see - (j * kPTile + 32 * w) : 0;  // positions of the block that exist
-      bool nan_any = false;
-      if (left < 32) {  // the end of the sequence (or a missing page): V is zero there, K may be anything
+    auto load_v = [&](int page) {
+      if ((unsigned)page >= (unsigned)a.c.n_pages) return;
+      const uint8_t* tile = tile_at(page);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u, tile += L::kBytes) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int p = 16 * u + 8 * n + 2 * tig;
-            const uint32_t keep = (p < left ? 0xFFFFu : 0u) | (p + 1 < left ? 0xFFFF0000u : 0u);
-            uint32_t* s = reinterpret_cast<uint32_t*>(vs[u]);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              vz[u][g][n] &= keep;
-              s[n * G + g] &= keep;
-            }
-          }
-      }
-      // NaN values of V become zeros here; the rows that see them learn of it through nan_groups
-      uint32_t bits = 0;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int v = 0; v < 2 * G / 4; ++v) {
+          vc[u][v] = ldnc16(tile + L::kV + v * 512 + lane * 16);
+          vs[u][v] = ldnc16(tile + L::kVs + v * 64 + tig * 16);
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            const uint32_t z = vz[u][g][n];
-            bits |= nan_half(z) || nan_half(z >> 16) ? 1u : 0u;
-          }
-      nan_any = __any_sync(0xFFFFFFFFu, bits != 0);
-      if (nan_any) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            uint32_t lo = 0, hi = 0;
-            uint32_t* s = reinterpret_cast<uint32_t*>(vs[u]);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const uint32_t z = vz[u][g][n];
-              const uint32_t drop = (nan_half(z) ? 0xFFFFu : 0u) | (nan_half(z >> 16) ? 0xFFFF0000u : 0u);
-              lo |= (nan_half(z) ? 1u : 0u) << g;
-              hi |= (nan_half(z >> 16) ? 1u : 0u) << g;
-              vz[u][g][n] &= ~drop;
-              s[n * G + g] &= ~drop;
-            }
-            if (gid == 0) {
-              sh.nan_groups[buf][32 * w + 16 * u + 8 * n + 2 * tig] = (uint8_t)lo;
-              sh.nan_groups[buf][32 * w + 16 * u + 8 * n + 2 * tig + 1] = (uint8_t)hi;
-            }
-          }
+          for (int g = 0; g < G; ++g)
+            vz[u][g][n] = __ldg(reinterpret_cast<const uint32_t*>(tile + L::kVz + g * 32 + n * 16 + tig * 4));
       }
-      if (lane == 0) sh.special[buf][w] = (page != -2 && !have ? 1u << w : 0u) | (nan_any ? 16u << w : 0u);
-      // K: row of position 16 u + 8 n + gid of the block (column order), 16 bytes per word
+    };
+    bool ok = true;
+    // K of tile j: row of position 16 u + 8 n + gid of the block (column order), 16 bytes per word
+    auto put_k = [&](int j, int page) {
+      const int buf = j & 1;
+      if (j >= 2) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.k_empty[buf], ((j >> 1) - 1) & 1, a.c.status));
+      if (!ok) return;
+      uint8_t* sk = skv + buf * 2 * PSmem<D>::kKV;
+      if (lane == 0) {
+        const bool bad = page != -2 && (unsigned)page >= (unsigned)a.c.n_pages;
+        sh.bad[buf][w] = bad;
+        if (bad) atomicOr(a.c.status, KV4_BAD_PAGE);
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -476,7 +452,49 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
             *reinterpret_cast<uint4*>(sk + (word >> 3) * 16384 + chunk_at(r, word & 7)) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-      // V transposed: row of value 32 g + 4 gid + i, 8 positions (16 bytes) per lane
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.k_full[buf]);
+    };
+    // V of tile j transposed: row of value 32 g + 4 gid + i, 8 positions (16 bytes) per lane
+    auto put_v = [&](int j, int page) {
+      const int buf = j & 1, p0 = j * kPTile + 32 * w;
+      const int left = (unsigned)page < (unsigned)a.c.n_pages ? see - p0 : 0;  // positions of the block that exist
+      uint32_t odd = 0;  // a NaN among the parameters
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int p = 16 * u + 8 * n + 2 * tig;
+          uint32_t* s = reinterpret_cast<uint32_t*>(vs[u]);
+          if (left < 32) {  // the end of the sequence (or a missing page): zeros
+            const uint32_t keep = (p < left ? 0xFFFFu : 0u) | (p + 1 < left ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              vz[u][g][n] &= keep;
+              s[n * G + g] &= keep;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) odd |= (uint32_t)(nan_half(vz[u][g][n]) || nan_half(vz[u][g][n] >> 16));
+        }
+      if (__any_sync(0xFFFFFFFFu, odd != 0)) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const uint32_t z = vz[u][g][n];
+              const int p = p0 + 16 * u + 8 * n + 2 * tig;
+              if (nan_half(z) || nan_half(z >> 16)) atomicMin(&sh.nan_first[g], nan_half(z) ? p : p + 1);
+              const uint32_t keep = (nan_half(z) ? 0u : 0xFFFFu) | (nan_half(z >> 16) ? 0u : 0xFFFF0000u);
+              vz[u][g][n] &= keep;
+              reinterpret_cast<uint32_t*>(vs[u])[n * G + g] &= keep;
+            }
+      }
+      if (j >= 2) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.v_empty[buf], ((j >> 1) - 1) & 1, a.c.status));
+      if (!ok) return;
+      uint8_t* sv = skv + buf * 2 * PSmem<D>::kKV + PSmem<D>::kKV;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint32_t v[4][4];  // [2 u + hf][value]
@@ -494,57 +512,85 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sh.kv_full[buf]);
-      if (j + 1 < n_max) load(j + 1);
+      mbar_arrive(&sh.v_full[buf]);
+    };
+    // K runs a tile ahead of V (its buffer is free as soon as the scores are done)
+    int page_k = look(0), page_v = page_k, page_next = look(1);
+    load_k(page_k);
+    load_v(page_v);
+    for (int j = -1; j < n_max && ok; ++j) {
+      if (j + 1 < n_max) {
+        put_k(j + 1, page_k);
+        page_k = page_next;
+        load_k(page_k);
+        page_next = look(j + 3);
+      }
+      if (j >= 0 && ok) {
+        put_v(j, page_v);
+        page_v = look(j + 1);
+        load_v(page_v);
+      }
     }
-  } else if (lane == 0 && n_max > 0) {
-    // ---------------- matrix instructions ----------------
-    bool ok = pwait(&sh.q_full, 0, a.c.status);
-    auto qk = [&](int t, int j) {
-      const uint32_t q = smem_u32(sq) + t * (D / 64) * 16384, k = smem_u32(skv) + (j & 1) * 2 * PSmem<D>::kKV;
+  } else if (n_max > 0) {
+    // ---------------- matrix instructions (the warp converged, one lane issues) ----------------
+    const int t = warp - 12, n = n_half[t];
+    const uint32_t one = elect_one();
+    const uint64_t dq = sw128_desc(smem_u32(sq) + t * (D / 64) * 16384), dk = sw128_desc(smem_u32(skv)),
+                   dv = sw128_desc(smem_u32(skv) + PSmem<D>::kKV);
+    constexpr uint32_t kBuf = 2 * PSmem<D>::kKV / 16;  // a buffer further, in the descriptor's 16-byte units
+    const uint32_t tms = tmem + t * 128, tmo = tmem + kO + t * D;
+    // scores of half i, and the product of its weights
+    auto qk = [&](int i) {
+      const uint64_t k = dk + (uint32_t)(i >> 1 & 1) * kBuf + (uint32_t)(i & 1) * 512;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        umma_f16(tmem + t * 128, sw128_desc(q + (i / 4) * 16384 + (i % 4) * 32),
-                 sw128_desc(k + (i / 4) * 16384 + (i % 4) * 32), kIdQK, i ? 1u : 0u);
-      umma_commit(&sh.s_full[t]);
+      for (int c = 0; c < D / 16; ++c)
+        mma_ss(one, tms + (i & 1) * 64, dq + (c / 4) * 1024 + (c % 4) * 2, k + (c / 4) * 1024 + (c % 4) * 2, kIdQK,
+               c ? 1u : 0u);
+      mma_commit(one, &sh.s_full[t][i & 1]);
+      if (i & 1 || i + 1 == n) mma_commit(one, &sh.k_empty[i >> 1 & 1]);  // the tile's last scores
     };
-    auto wv = [&](int t, int j) {
-      const uint32_t v = smem_u32(skv) + (j & 1) * 2 * PSmem<D>::kKV + PSmem<D>::kKV;
+    auto wv = [&](int i) {
+      const uint64_t v = dv + (uint32_t)(i >> 1 & 1) * kBuf + (uint32_t)(i & 1) * (D * 8);
 #pragma unroll
-      for (int i = 0; i < kPTile / 16; ++i)
-        umma_f16_ts(tmem + 256 + t * D, tmem + t * 128 + 8 * i, sw128_desc(v + (i / 4) * (D * 128) + (i % 4) * 32), kIdWV,
-                    j || i ? 1u : 0u);
+      for (int c = 0; c < 4; ++c) mma_ts(one, tmo, tms + (i & 1) * 64 + 8 * c, v + c * 2, kIdWV, i || c ? 1u : 0u);
+      mma_commit(one, &sh.wv_done[t]);
+      if (i & 1 || i + 1 == n) mma_commit(one, &sh.v_empty[i >> 1 & 1]);
+      if (i + 1 == n) mma_commit(one, &sh.o_full[t]);
     };
-    ok = ok && pwait(&sh.kv_full[0], 0, a.c.status);
-    if (ok) {
+    auto ready = [&](uint64_t* bar, int j) {
+      const bool r = __all_sync(0xFFFFFFFFu, kv4_wait(bar + (j & 1), (j >> 1) & 1, a.c.status));
       tc_fence_after();
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (n_tiles[t] > 0) qk(t, 0);
-    }
-    for (int j = 0; j < n_max && ok; ++j) {
-      bool next = false;  // tile j + 1 has been waited for
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (j >= n_tiles[t] || !ok) continue;
-        ok = pwait(&sh.w_full[t], j & 1, a.c.status);
+      return r;
+    };
+    bool ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.q_full, 0, a.c.status));
+    if (n > 0) {
+      ok = ok && ready(sh.k_full, 0);
+      if (ok) {
+        qk(0);
+        if (n > 1) qk(1);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        if (!(i & 1)) ok = ready(sh.v_full, i >> 1);
+        if (ok) ok = ready(sh.w_full[t], i);
         if (!ok) break;
-        tc_fence_after();
-        wv(t, j);
-        if (j + 1 == n_tiles[t]) umma_commit(&sh.o_full[t]);
-        if (t == 1 || n_tiles[1] <= j) umma_commit(&sh.kv_empty[j & 1]);  // the last product of this tile
-        if (j + 1 < n_tiles[t]) {
-          if (!next) ok = pwait(&sh.kv_full[(j + 1) & 1], ((j + 1) >> 1) & 1, a.c.status);
-          next = true;
-          if (!ok) break;
-          tc_fence_after();
-          qk(t, j + 1);
+        wv(i);
+        if (i + 2 < n) {
+          if (!(i & 1)) ok = ready(sh.k_full, (i + 2) >> 1);
+          if (ok) qk(i + 2);
         }
       }
     }
+    // tiles that only the other query tile sees: this one lets go of them as they come
+    for (int j = (n + 1) / 2; j < n_max && ok; ++j) {
+      ok = ready(sh.k_full, j);
+      if (ok && lane == 0) mbar_arrive(&sh.k_empty[j & 1]);
+      ok = ok && ready(sh.v_full, j);
+      if (ok && lane == 0) mbar_arrive(&sh.v_empty[j & 1]);
+      __syncwarp();
+    }
     if (!ok) {  // let what was issued finish before the memory goes
-      umma_commit(&sh.drained);
-      pwait(&sh.drained, 0, a.c.status);
+      mma_commit(one, &sh.drained[t]);
+      kv4_wait(&sh.drained[t], 0, a.c.status);
     }
   }
   __syncwarp();
