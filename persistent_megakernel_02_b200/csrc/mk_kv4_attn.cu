@@ -65,6 +65,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {  // at the rate of a maximum of two
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -142,26 +147,29 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   // ---- ring of bulk copies: this warp's stage i is stage s0 + warp + kWarps i ----
   const int n_stages = p0 < p1 ? (p1 - 1) / kStagePos - s0 + 1 : 0;
   const int mine = n_stages > warp ? (n_stages - warp - 1) / kWarps + 1 : 0;
-  auto issue = [&](int i) {  // every lane calls
+  const int first = s0 + warp, last = s0 + n_stages - 1;
+  const uint32_t last_bytes = (uint32_t)((p1 - last * kStagePos + kKv4Tile - 1) / kKv4Tile) * L::kBytes;
+  const uint64_t page_stride = (uint64_t)a.c.n_kv_heads * (kKv4Tiles * L::kBytes);
+  const uint8_t* base = static_cast<const uint8_t*>(a.c.pool) + (uint64_t)a.layer * a.c.n_pages * page_stride +
+                        (uint64_t)head * (kKv4Tiles * L::kBytes);
+  auto issue = [&](int i, int slot) {  // every lane calls
     if (i > 0 && (i & 31) == 0) {
       const int j = i + lane;
-      page_id = j < mine ? table[(s0 + warp + kWarps * j) / kStagesPerPage] : 0;
+      page_id = j < mine ? table[(first + kWarps * j) / kStagesPerPage] : 0;
     }
     const int page = __shfl_sync(0xFFFFFFFFu, page_id, i & 31);
     if (lane == 0) {
-      const int s = s0 + warp + kWarps * i, slot = i % kStages;
+      const int s = first + kWarps * i;
       const bool bad = (unsigned)page >= (unsigned)a.c.n_pages;
       slot_bad[warp][slot] = bad;
       if (bad) {
         atomicOr(a.c.status, KV4_BAD_PAGE);
         mbar_arrive(&full[warp][slot]);
       } else {
-        const int tiles = min(kTilesPerStage, (p1 - s * kStagePos + kKv4Tile - 1) / kKv4Tile);
-        const size_t tile = (((size_t)a.layer * a.c.n_pages + page) * a.c.n_kv_heads + head) * kKv4Tiles +
-                            (s % kStagesPerPage) * kTilesPerStage;
-        mbar_arrive_expect_tx(&full[warp][slot], tiles * L::kBytes);
-        bulk_g2s_plain(ring + slot * kStageBytes, static_cast<const uint8_t*>(a.c.pool) + tile * L::kBytes,
-                       tiles * L::kBytes, &full[warp][slot]);
+        const uint32_t bytes = s == last ? last_bytes : (uint32_t)kStageBytes;
+        mbar_arrive_expect_tx(&full[warp][slot], bytes);
+        bulk_g2s_plain(ring + slot * kStageBytes, base + (uint64_t)(uint32_t)page * page_stride + (s % kStagesPerPage) * kStageBytes,
+                       bytes, &full[warp][slot]);
       }
     }
   };
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     fence_barrier_init();
   }
   __syncwarp();
-  for (int i = 0; i < kStages && i < mine; ++i) issue(i);
+  for (int i = 0; i < kStages && i < mine; ++i) issue(i, i);
 
   // ---- queries: operand order of the codes, scaled by a power of two per row ----
   // [16 rows][group][k16 step][a0..a3].  With 8 rows of 16-bit queries rows 8..15 of the
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
             if (p >= lim[t] || p >= p1) s[t][u][i] = -INFINITY;
           }
         }
-        r[u] = fmaxf(fmaxf(s[t][u][0], s[t][u][1]), fmaxf(s[t][u][2], s[t][u][3]));
+        r[u] = max3(fmaxf(s[t][u][0], s[t][u][1]), s[t][u][2], s[t][u][3]);
       }
 #pragma unroll
       for (int u = 1; u < SUB; ++u) r[0] = fmaxf(r[0], r[u]);
@@ -482,22 +490,28 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   };
 
   bool alive = true;
+  const int clear = min(see_all, p1);  // positions that need no mask
+  int slot = 0;
+  uint32_t parity = 0;
   for (int i = 0; i < mine; ++i) {
-    const int slot = i % kStages, s = s0 + warp + kWarps * i;
-    alive = __all_sync(0xFFFFFFFFu, kv4_wait(&full[warp][slot], (i / kStages) & 1, a.c.status));
+    alive = __all_sync(0xFFFFFFFFu, kv4_wait(&full[warp][slot], parity, a.c.status));
     if (!alive) break;
     if (!slot_bad[warp][slot]) {
       const uint8_t* tiles = ring + slot * kStageBytes;
-      const int pos = s * kStagePos;
+      int at = (first + kWarps * i) * kStagePos;
+      const int end = min(p1, at + kStagePos);
 #pragma unroll 1
-      for (int u = 0; u < kTilesPerStage && pos + 16 * u < p1; u += SUB) {
-        const int at = pos + 16 * u;
-        if (at + 16 * SUB <= min(see_all, p1)) step(tiles + u * L::kBytes, at, std::false_type{});
-        else step(tiles + u * L::kBytes, at, std::true_type{});
+      for (; at < end; at += 16 * SUB, tiles += SUB * L::kBytes) {
+        if (at + 16 * SUB <= clear) step(tiles, at, std::false_type{});
+        else step(tiles, at, std::true_type{});
       }
     }
     __syncwarp();
-    if (i + kStages < mine) issue(i + kStages);
+    if (i + kStages < mine) issue(i + kStages, slot);
+    if (++slot == kStages) {
+      slot = 0;
+      parity ^= 1u;
+    }
   }
   if (!alive) {  // copies still in flight must land before the CTA's shared memory goes
     for (int i = 0; i < kStages; ++i) kv4_wait(&full[warp][i], 0, a.c.status), kv4_wait(&full[warp][i], 1, a.c.status);
