@@ -26,8 +26,9 @@ struct Kv4Attn {
   float scale_log2;  // scale * log2(e)
 };
 
-// Opt-in to more than 48 KiB of shared memory, once per kernel and device.
-bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready);
+// Opt-in to more than 48 KiB of shared memory (and to clusters of more than 8 CTAs), once
+// per kernel and device.
+bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready, bool large_cluster = false);
 
 // Attention of many query rows of 16-bit types (mk_kv4_prompt.cu).
 mk_status kv4_prompt(const Kv4Attn& a, int32_t dtype, cudaStream_t s);

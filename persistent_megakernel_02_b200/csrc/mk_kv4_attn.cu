@@ -19,6 +19,7 @@
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
 // merged.  Splits along the positions, where rows are few, are joined by a second
 // small kernel.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -97,7 +98,7 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 //   outputs  value 32 g + 4 gid + 2 j + {0, 1} of rows 2 tig, 2 tig + 1
 // 32-bit calls split queries and weights into two fp16 parts: the queries' low parts
 // are rows 8..15 of the same mma, the weights' take a second one.
-template <int D, class T, int NT>
+template <int D, class T, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const AttnArgs a) {
   using L = Kv4<D>;
   constexpr int G = L::G;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   const int see_all = start + row0 / a.rep + 1;                // positions every row of the tile sees
   const int see_any = max(0, start + last_row / a.rep + 1);    // positions some row sees
   const int p1 = min(see_any, p0 + a.split_len);
-  if (p0 >= p1 && split > 0) return;  // the merge takes only the splits that hold something
+  if (!CLUSTER && p0 >= p1 && split > 0) return;  // the join takes only the splits that hold something
 
   // ---- ring of bulk copies: this warp's stage i is stage s0 + warp + kWarps i ----
   const int n_stages = p0 < p1 ? (p1 - 1) / kStagePos - s0 + 1 : 0;
@@ -521,6 +522,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   __syncthreads();
   float* ob = reinterpret_cast<float*>(smem);            // [warp][row][D]
   float* ml = ob + kWarps * kRows * D;                   // [warp][row][2]
+  float* own = ml + kWarps * kRows * 2;                  // [row][D + 4], of a cluster's CTA
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     if (tig == 0) ml[(warp * kRows + 8 * t + gid) * 2] = ref[t];
@@ -560,7 +562,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int i = 0; i < 8; ++i) x[i] = fmaf(f, src[i], x[i]);
     }
     if (a.n_split > 1) {
-      float* dst = a.part + ((size_t)blockIdx.x * kRows + r) * (D + 4);
+      // for the join: in the workspace, or in this CTA's shared memory for its cluster
+      float* dst = CLUSTER ? own + r * (D + 4) : a.part + ((size_t)blockIdx.x * kRows + r) * (D + 4);
       store8<float>(dst + 4 + 8 * w8, x);
       if (w8 == 0) *reinterpret_cast<float2*>(dst) = make_float2(top, sum);
     } else {
@@ -569,6 +572,36 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int i = 0; i < 8; ++i) x[i] *= inv;
       store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
     }
+  }
+  if constexpr (CLUSTER) {
+    // the cluster's CTAs are the splits: each joins a share of the rows out of all their
+    // shared memories
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    for (int e = threadIdx.x * a.n_split + split; e < kRows * (D / 8); e += kThreadsA * a.n_split) {
+      const int r = e / (D / 8), w8 = e % (D / 8), row = row0 + r;
+      if (row > last_row) break;
+      float top = -INFINITY;
+      for (int q = 0; q < a.n_split; ++q) top = fmaxf(top, cluster.map_shared_rank(own, q)[r * (D + 4)]);
+      float sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int q = 0; q < a.n_split; ++q) {
+        const float* p = cluster.map_shared_rank(own, q) + r * (D + 4);
+        const float2 ml = *reinterpret_cast<const float2*>(p);
+        const float4 u = *reinterpret_cast<const float4*>(p + 4 + 8 * w8), v = *reinterpret_cast<const float4*>(p + 8 + 8 * w8);
+        const float f = top == -INFINITY ? 0.f : ex2(ml.x - top);
+        const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        sum = fmaf(f, ml.y, sum);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(f, y[i], x[i]);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= inv;
+      store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
+    }
+    cluster.sync();  // no CTA leaves while another reads its memory
   }
 }
 
@@ -634,20 +667,31 @@ __global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
 struct Plan {
   bool prompt;  // many rows of 16-bit queries: the tcgen05 kernel, unsplit
   int nt, n_rt, n_split, split_len;
+  bool cluster;  // the splits of a row tile are a cluster and join in shared memory
   long long ctas;
   int64_t part_bytes;
 };
 
+// SMs of the current device (looked up once per device), 0 on an error.
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // How a call is cut up, from its bounds alone.
 mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dtype, Plan* p) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MK_ERR_CUDA;
+  const int sms = sm_count();
+  if (sms <= 0) return MK_ERR_CUDA;
   const long long rows = std::max<long long>(b->max_new, 1) * rep;  // 0: still looks at the spans
   p->prompt = dtype != 2 && rows >= 128;
   if (p->prompt) {
     p->n_split = 1;
+    p->cluster = false;
     p->part_bytes = 0;
     return MK_OK;
   }
@@ -665,38 +709,62 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   long long n_split = 1;
   if (base > 0)
     n_split = std::max({1ll, std::min(2ll * sms / base, pages / kWarps), std::min(8ll * sms / base, pages / 32)});
+  // Where the splits fill the SMs about once, up to 16 of them are a cluster (a power of
+  // two): no workspace and no second launch (eight lanes of about 1000 positions in fp32:
+  // 9.6 -> 8.3 us).  Longer grids lose by it, a cluster's CTAs being placed together (64
+  // sequences of up to 16384 positions: 152 -> 204 us).
+  p->cluster = n_split > 1 && n_split <= 16 && base * n_split <= 2ll * sms;
+  if (p->cluster) {
+    long long c = 2;
+    while (2 * c <= std::min(n_split, 16ll)) c *= 2;
+    n_split = c;
+  }
   const long long per = std::max(1ll, (pages + n_split - 1) / n_split);
-  n_split = std::max(1ll, (pages + per - 1) / per);
+  if (!p->cluster) n_split = std::max(1ll, (pages + per - 1) / per);
   p->n_rt = (int)n_rt;
   p->n_split = (int)n_split;
   p->split_len = (int)std::min<long long>(per * unit, 0x7FFFFFC0);
   p->ctas = base * n_split;
   if (p->ctas > 0x7FFFFFFF / 64) return MK_ERR_UNSUPPORTED;
-  p->part_bytes = n_split > 1 ? p->ctas * 8 * p->nt * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
+  p->part_bytes = n_split > 1 && !p->cluster ? p->ctas * 8 * p->nt * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
   return MK_OK;
 }
 
 template <int D, class T, int NT>
 mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
-  constexpr int kMerge = kWarps * 8 * NT * (D + 2) * 4;
+  constexpr int kMerge = 8 * NT * (kWarps * (D + 2) + D + 4) * 4;
   constexpr int kSmem = kMerge > kWarps * kStages * kStageBytes ? kMerge : kWarps * kStages * kStageBytes;
-  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
-  if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT>), kSmem, &ready)) return MK_ERR_CUDA;
-  attn_few<D, T, NT><<<(unsigned)p.ctas, kThreadsA, kSmem, s>>>(a);
+  static std::atomic<uint64_t> ready{0}, ready_cluster{0};  // devices whose attributes are set
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  cfg.blockDim = dim3(kThreadsA);
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  if (p.cluster) {
+    const void* kernel = reinterpret_cast<const void*>(attn_few<D, T, NT, true>);
+    if (!kv4_allow_smem(kernel, kSmem, &ready_cluster, true)) return MK_ERR_CUDA;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.n_split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, true>, a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  }
+  if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT, false>), kSmem, &ready, false)) return MK_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, false>, a) != cudaSuccess) return MK_ERR_CUDA;
   if (p.n_split > 1) {
     // launched while the splits run (its first loads wait for them)
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.ctas / p.n_split * 8 * NT));
     cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
+    cfg.dynamicSmemBytes = 0;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, attn_join<D, T, NT>, a) != cudaSuccess) return MK_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return MK_OK;
 }
 
 template <int D, class T>
@@ -718,12 +786,14 @@ mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_bat
 
 }  // namespace
 
-bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
+bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready, bool large_cluster) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (ready->load(std::memory_order_relaxed) & bit) return true;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (large_cluster && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return false;
   ready->fetch_or(bit, std::memory_order_relaxed);
   return true;
 }

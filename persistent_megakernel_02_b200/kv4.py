@@ -19,6 +19,12 @@ import torch
 
 from . import MkError, MkKv4Batch, MkKv4CacheStruct, MkKv4Rows, _check, lib
 
+# the raw forms of torch.cuda.current_device and current_stream, where this torch has them
+# (the public ones cost about 2 us of a call of 5)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 PAGE = 64
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -101,23 +107,25 @@ class Kv4Cache:
                         max_new, max_len)
 
     def _launch(self, what, stream):
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             _bad(what, f"the cache is not on the current CUDA device ({torch.cuda.current_device()})")
         if stream is None:
-            return torch.cuda.current_stream(self._index).cuda_stream
+            return _current_stream(self._index)
         return getattr(stream, "cuda_stream", stream)
 
     def _rows(self, what, name, t, heads, batch, dtype):
+        if (t.shape == (batch.n_rows, heads, self.head_dim) and t.dtype is dtype and dtype in _DTYPES
+                and t.get_device() == self._index):
+            rs, hs, es = t.stride()
+            if es == 1:
+                return MkKv4Rows(t.data_ptr(), rs, hs)
         if t.shape != (batch.n_rows, heads, self.head_dim):
             _bad(what, f"{name} must have shape ({batch.n_rows}, {heads}, {self.head_dim}), got {tuple(t.shape)}")
         if t.dtype is not dtype or dtype not in _DTYPES:
             _bad(what, f"{name} must be bfloat16, float16 or float32, the same type for every tensor; got {t.dtype}")
         if t.get_device() != self._index:
             _bad(what, f"{name} must be on {self.device}")
-        rs, hs, es = t.stride()
-        if es != 1:
-            _bad(what, f"the last dimension of {name} must be contiguous")
-        return MkKv4Rows(t.data_ptr(), rs, hs)
+        _bad(what, f"the last dimension of {name} must be contiguous")
 
     def _kv(self, fn, what, layer, k, v, batch, stream):
         dtype = k.dtype
