@@ -72,13 +72,13 @@ __device__ __forceinline__ TileJob tile_job(const mk_kv4_cache& c, const mk_kv4_
 
 constexpr int kRowWarps = 4;  // warps per CTA, each with work of its own
 
-// A warp takes the K rows or the V rows (`which`) of one tile of one kv head: a lane has 8
-// neighbouring values of a row (4 neighbouring lanes share a group), and a warp-wide
-// access covers kStep rows.  The place of row r0 + rl in the tile is that of r0 plus that
-// of rl, so only the part of rl is computed at run time.
+// A warp takes one tile of one kv head, K and then V: a lane has 8 neighbouring values of a
+// row (4 neighbouring lanes share a group), and a warp-wide access covers kStep rows.  The
+// place of row r0 + rl in the tile is that of r0 plus that of rl, so only the part of rl
+// is computed at run time.
 template <int D, class T, class Rows>
 __device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head,
-                                              int which, uint8_t* image) {
+                                              uint8_t* image) {
   using L = Kv4<D>;
   constexpr int kChunks = D / 8, kStep = 32 / kChunks, kItems = kKv4Tile / kStep;
   const int lane = threadIdx.x & 31, w = lane % kChunks, rl = lane / kChunks;
@@ -92,13 +92,11 @@ __device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJ
   // A whole tile's codes and parameters are put together in shared memory and stored with
   // 16-byte stores: codes of K or of V, 8 D bytes, then scales and minima, 2 D bytes.
   // Part of a tile (a new token) goes out value by value; the other rows stay as they are.
-  uint8_t* codes_base = whole ? image : out + (which ? L::kV : 0);
-  uint8_t* param_base = whole ? image + 8 * D : out + (which ? L::kVs : L::kKs);
-  uint8_t* codes_at = codes_base + (which ? L::v_unit(rl, 2 * w) - L::kV : L::k_word(rl, w));
-  auto load = [&](Raw8<T> (&raw)[4], int b0) {
+  auto load = [&](Raw8<T> (&raw)[4], int b0) {  // accesses b0 .. b0 + 3: K has 0 .. kItems - 1, V the next
+    const int which = b0 >= kItems;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = (b0 + i) * kStep + rl;
+      const int r = (b0 - which * kItems + i) * kStep + rl;
       raw[i] = Raw8<T>{};
       if (r >= skip && r < stop)
         raw[i] = load_raw8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head,
@@ -108,61 +106,72 @@ __device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJ
   Raw8<T> next[4];
   load(next, 0);
 #pragma unroll 1
-  for (int b0 = 0; b0 < kItems; b0 += 4) {  // four accesses at a time, the next four on their way
-    Raw8<T> raw[4];
-    float2 e[4];
+  for (int which = 0; which < 2; ++which) {
+    uint8_t* codes_base = whole ? image : out + (which ? L::kV : 0);
+    uint8_t* param_base = whole ? image + 8 * D : out + (which ? L::kVs : L::kKs);
+    uint8_t* codes_at = codes_base + (which ? L::v_unit(rl, 2 * w) - L::kV : L::k_word(rl, w));
+#pragma unroll 1
+    for (int b0 = 0; b0 < kItems; b0 += 4) {  // four accesses at a time, the next four on their way
+      Raw8<T> raw[4];
+      float2 e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = next[i];
-    if (b0 + 4 < kItems) load(next, b0 + 4);
+      for (int i = 0; i < 4; ++i) raw[i] = next[i];
+      if (which * kItems + b0 + 4 < 2 * kItems) load(next, which * kItems + b0 + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = extent8(raw[i]);
-    // lane k of a group's quad has the parameters of access k
-    const float lo = quad_scatter_min(e[0].x, e[1].x, e[2].x, e[3].x, lane);
-    const float hi = -quad_scatter_min(e[0].y, e[1].y, e[2].y, e[3].y, lane);
-    const uint32_t mine = kv4_params(lo, hi);
-    const float s = h_lo(mine), inv_mine = s > 0.f ? __frcp_rn(s) : 0.f;
-    {
-      const int r = (b0 + (lane & 3)) * kStep + rl, g = w / 4;
-      if (r >= skip && r < stop) {
-        *reinterpret_cast<uint16_t*>(param_base + L::scale(r, g)) = (uint16_t)mine;
-        *reinterpret_cast<uint16_t*>(param_base + (which ? L::v_min(r, g) - L::kVs : L::k_min(r, g) - L::kKs)) =
-            (uint16_t)(mine >> 16);
+      for (int i = 0; i < 4; ++i) e[i] = extent8(raw[i]);
+      // lane k of a group's quad has the parameters of access k
+      const float lo = quad_scatter_min(e[0].x, e[1].x, e[2].x, e[3].x, lane);
+      const float hi = -quad_scatter_min(e[0].y, e[1].y, e[2].y, e[3].y, lane);
+      const uint32_t mine = kv4_params(lo, hi);
+      const float s = h_lo(mine), inv_mine = s > 0.f ? __frcp_rn(s) : 0.f;
+      {
+        const int r = (b0 + (lane & 3)) * kStep + rl, g = w / 4;
+        if (r >= skip && r < stop) {
+          *reinterpret_cast<uint16_t*>(param_base + L::scale(r, g)) = (uint16_t)mine;
+          *reinterpret_cast<uint16_t*>(param_base + (which ? L::v_min(r, g) - L::kVs : L::k_min(r, g) - L::kKs)) =
+              (uint16_t)(mine >> 16);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t params = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) | i);
+        const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, (lane & ~3) | i);
+        float x[8];
+        unpack8(raw[i], x);
+        const uint32_t codes = kv4_codes(x, params, inv);
+        const int r0 = (b0 + i) * kStep, r = r0 + rl;
+        if (r < skip || r >= stop) continue;
+        if (which == 0) {
+          *reinterpret_cast<uint32_t*>(codes_at + L::k_word(r0, 0)) = codes;
+        } else {
+          constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
+          uint8_t* at = codes_at + (L::v_unit(r0, 0) - L::kV);
+          *reinterpret_cast<uint16_t*>(at) = (uint16_t)codes;
+          *reinterpret_cast<uint16_t*>(at + kNext) = (uint16_t)(codes >> 16);
+        }
       }
     }
+    if (!whole) continue;
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t params = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) | i);
-      const float inv = __shfl_sync(0xFFFFFFFFu, inv_mine, (lane & ~3) | i);
-      float x[8];
-      unpack8(raw[i], x);
-      const uint32_t codes = kv4_codes(x, params, inv);
-      const int r0 = (b0 + i) * kStep, r = r0 + rl;
-      if (r < skip || r >= stop) continue;
-      if (which == 0) {
-        *reinterpret_cast<uint32_t*>(codes_at + L::k_word(r0, 0)) = codes;
-      } else {
-        constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
-        uint8_t* at = codes_at + (L::v_unit(r0, 0) - L::kV);
-        *reinterpret_cast<uint16_t*>(at) = (uint16_t)codes;
-        *reinterpret_cast<uint16_t*>(at + kNext) = (uint16_t)(codes >> 16);
-      }
-    }
+    for (int e = lane; e < 8 * D / 16; e += 32)
+      reinterpret_cast<uint4*>(out + (which ? L::kV : 0))[e] = reinterpret_cast<const uint4*>(image)[e];
+    if (lane < 2 * D / 16)
+      reinterpret_cast<uint4*>(out + (which ? L::kVs : L::kKs))[lane] =
+          reinterpret_cast<const uint4*>(image + 8 * D)[lane];
+    __syncwarp();
   }
-  if (!whole) return;
-  __syncwarp();
-#pragma unroll
-  for (int e = lane; e < 8 * D / 16; e += 32)
-    reinterpret_cast<uint4*>(out + (which ? L::kV : 0))[e] = reinterpret_cast<const uint4*>(image)[e];
-  if (lane < 2 * D / 16)
-    reinterpret_cast<uint4*>(out + (which ? L::kVs : L::kKs))[lane] =
-        reinterpret_cast<const uint4*>(image + 8 * D)[lane];
 }
 
-// The way back: codes and parameters come in with 16-byte loads, and a lane puts out 8
-// neighbouring values of a row.
+// The way back: the tile comes in with 16-byte loads, and a lane puts out 8 neighbouring
+// values of a row.  32-bit rows are twice as long to write, so a warp writes K or V only
+// (eight sequences of 517 to 1420 rows, 8 heads of 128: 18.0 us, both 20.1; 16-bit rows
+// gain by both, 8192 rows of 64 6.5 -> 5.1 us).
+template <class T>
+constexpr int kReadParts = sizeof(T) == 4 ? 2 : 1;
 template <int D, class T, class Rows>
 __device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head,
-                                          int which, uint8_t* image) {
+                                          int part_of, uint8_t* image) {
   using L = Kv4<D>;
   constexpr int kChunks = D / 8, kStep = 32 / kChunks, kItems = kKv4Tile / kStep;
   const int lane = threadIdx.x & 31, w = lane % kChunks, rl = lane / kChunks;
@@ -171,67 +180,73 @@ __device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& 
     if (lane == 0) atomicOr(c.status, KV4_BAD_PAGE);
     return;
   }
+  uint4 part[(L::kBytes / 16 + 31) / 32];
 #pragma unroll
-  for (int e = lane; e < 8 * D / 16; e += 32)
-    reinterpret_cast<uint4*>(image)[e] = reinterpret_cast<const uint4*>(src + (which ? L::kV : 0))[e];
-  if (lane < 2 * D / 16)
-    reinterpret_cast<uint4*>(image + 8 * D)[lane] =
-        reinterpret_cast<const uint4*>(src + (which ? L::kVs : L::kKs))[lane];
+  for (int i = 0; i * 32 < L::kBytes / 16; ++i)
+    if (lane + 32 * i < L::kBytes / 16) part[i] = reinterpret_cast<const uint4*>(src)[lane + 32 * i];
+#pragma unroll
+  for (int i = 0; i * 32 < L::kBytes / 16; ++i)
+    if (lane + 32 * i < L::kBytes / 16) reinterpret_cast<uint4*>(image)[lane + 32 * i] = part[i];
   __syncwarp();
-  const uint8_t* codes_at = image + (which ? L::v_unit(rl, 2 * w) - L::kV : L::k_word(rl, w));
-  const uint8_t* scale_at = image + 8 * D + L::scale(rl, w / 4);
-  const uint8_t* min_at = image + 8 * D + (which ? L::v_min(rl, w / 4) - L::kVs : L::k_min(rl, w / 4) - L::kKs);
-  const int skip = j.first - j.tile * kKv4Tile;
+  const int skip = j.first - j.tile * kKv4Tile, stop = skip + j.end - j.first;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    const int r = i * kStep + rl;
-    uint32_t codes;
-    if (which == 0) {
-      codes = *reinterpret_cast<const uint32_t*>(codes_at + L::k_word(i * kStep, 0));
-    } else {
-      constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
-      const uint8_t* at = codes_at + (L::v_unit(i * kStep, 0) - L::kV);
-      codes = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + kNext) << 16;
+  for (int which = 0; which < 2; ++which) {
+    if (kReadParts<T> == 2 && which != part_of) continue;
+    const uint8_t* codes_at = image + (which ? L::v_unit(rl, 2 * w) : L::k_word(rl, w));
+    const uint8_t* scale_at = image + (which ? L::kVs : L::kKs) + L::scale(rl, w / 4);
+    const uint8_t* min_at = image + (which ? L::v_min(rl, w / 4) : L::k_min(rl, w / 4));
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int r = i * kStep + rl;
+      uint32_t codes;
+      if (which == 0) {
+        codes = *reinterpret_cast<const uint32_t*>(codes_at + L::k_word(i * kStep, 0));
+      } else {
+        constexpr int kNext = L::v_unit(0, 1) - L::v_unit(0, 0);
+        const uint8_t* at = codes_at + (L::v_unit(i * kStep, 0) - L::kV);
+        codes = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + kNext) << 16;
+      }
+      const uint32_t params =
+          *reinterpret_cast<const uint16_t*>(scale_at + L::scale(i * kStep, 0)) |
+          (uint32_t)*reinterpret_cast<const uint16_t*>(
+              min_at + (which ? L::v_min(i * kStep, 0) - L::kVz : L::k_min(i * kStep, 0) - L::kKz)) << 16;
+      float x[8];
+      kv4_values(codes, h_lo(params), h_hi(params), x);
+      if (r >= skip && r < stop)
+        store8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head, c.n_kv_heads) +
+                      w * 8 * sizeof(T), x);
     }
-    const uint32_t params =
-        *reinterpret_cast<const uint16_t*>(scale_at + L::scale(i * kStep, 0)) |
-        (uint32_t)*reinterpret_cast<const uint16_t*>(
-            min_at + (which ? L::v_min(i * kStep, 0) - L::kVz : L::k_min(i * kStep, 0) - L::kKz)) << 16;
-    float x[8];
-    kv4_values(codes, h_lo(params), h_hi(params), x);
-    if (r >= skip && r < skip + j.end - j.first)
-      store8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head, c.n_kv_heads) +
-                    w * 8 * sizeof(T), x);
   }
 }
 
 template <int D, class T, bool WRITE, class Rows>
-__device__ __forceinline__ void do_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head, int which) {
-  __shared__ __align__(16) uint8_t image[kRowWarps][10 * D];
-  if (WRITE) quantise_tile<D, T>(c, j, rows, head, which, image[threadIdx.x >> 5]);
-  else read_tile<D, T>(c, j, rows, head, which, image[threadIdx.x >> 5]);
+__device__ __forceinline__ void do_tile(const mk_kv4_cache& c, const TileJob& j, const Rows& rows, int head, int part) {
+  __shared__ __align__(16) uint8_t image[kRowWarps][WRITE ? 10 * D : 20 * D];
+  if (WRITE) quantise_tile<D, T>(c, j, rows, head, image[threadIdx.x >> 5]);
+  else read_tile<D, T>(c, j, rows, head, part, image[threadIdx.x >> 5]);
 }
 
-// Warp g of the grid: kv head g % n_kv_heads, then K or V, then the slot, so neighbouring
-// warps are at neighbouring heads of the same rows.
+// Warp g of the grid: kv head g % n_kv_heads, then K or V where they are apart, then the
+// slot, so neighbouring warps are at neighbouring heads of the same rows.
 template <int D, class T, bool WRITE>
 __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
     rows_kernel(mk_kv4_cache c, int layer, mk_kv4_batch b, BatchRows rows, int n_slots) {
   const long long g = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int head = (int)(g % c.n_kv_heads), which = (int)(g / c.n_kv_heads & 1);
-  const int slot = (int)(g / (2 * c.n_kv_heads));
+  constexpr int kParts = WRITE ? 1 : kReadParts<T>;
+  const int head = (int)(g % c.n_kv_heads), part = (int)(g / c.n_kv_heads % kParts);
+  const int slot = (int)(g / (c.n_kv_heads * kParts));
   if (slot >= n_slots) return;
   const TileJob j = tile_job(c, b, layer, slot);
-  if (j.ok) do_tile<D, T, WRITE>(c, j, rows, head, which);
+  if (j.ok) do_tile<D, T, WRITE>(c, j, rows, head, part);
 }
 
-// Positions start .. start + n - 1 of a handle's slot: warps over (tile, K or V, kv head),
-// grid.y over the layers.
+// Positions start .. start + n - 1 of a handle's slot: warps over (tile, kv head), grid.y
+// over the layers.
 template <int D, class T, bool WRITE>
 __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
     slot_kernel(mk_kv4_cache c, SlotRows rows, const int32_t* table_row, int start, int n, int n_tiles) {
   const int g = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int head = g % c.n_kv_heads, which = g / c.n_kv_heads & 1, t = g / (2 * c.n_kv_heads);
+  const int head = g % c.n_kv_heads, t = g / c.n_kv_heads;
   if (t >= n_tiles) return;
   TileJob j;
   j.tile = start / kKv4Tile + t;
@@ -240,7 +255,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
   j.row0 = 0;
   j.layer = blockIdx.y;
   j.table = table_row;
-  do_tile<D, T, WRITE>(c, j, rows, head, which);
+  do_tile<D, T, WRITE>(c, j, rows, head, 0);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -265,7 +280,8 @@ mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, 
     rows.head[i] = kv[i]->head_stride * size;
   }
   const long long slots = b->n_rows / kKv4Tile + 2ll * b->n_seqs;
-  const long long ctas = (2 * slots * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
+  const int parts = WRITE || dtype != 2 ? 1 : kReadParts<float>;
+  const long long ctas = (slots * c->n_kv_heads * parts + kRowWarps - 1) / kRowWarps;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 #define MK_KV4_ROWS(D, T) rows_kernel<D, T, WRITE><<<(unsigned)ctas, 32 * kRowWarps, 0, s>>>(*c, layer, *b, rows, (int)slots)
@@ -320,7 +336,7 @@ mk_status kv4_slot(bool write, const mk_kv4_cache* c, void* kv, const int* slot_
                    bool fp16, const int32_t* table_row, int start, int n, cudaStream_t s) {
   const SlotRows rows{static_cast<char*>(kv), slot_table, n_phys_pages, PL};
   const int n_tiles = (start + n - 1) / kKv4Tile - start / kKv4Tile + 1;
-  const long long ctas = (2ll * n_tiles * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
+  const long long ctas = ((long long)n_tiles * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
   if (ctas * kRowWarps > 0x7FFFFFFF || c->n_layers > 65535) return MK_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)ctas, c->n_layers);
 #define MK_KV4_SLOT(D, T)                                                                                        \
