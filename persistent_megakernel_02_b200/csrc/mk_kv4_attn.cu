@@ -3,11 +3,11 @@
 //
 // Mathematics.  With K = z + s c per group g of 32 values, a score is
 //   q . K = sum_g s_g (q_g . c_g) + sum_g z_g (sum of q_g),
-// so the codes enter the matrix instructions as they are: a 4-bit code in the low bits
-// of an fp16 word is the subnormal c 2^-24 (or 16 c 2^-24 from the next nibble, with
-// the query divided by 16 instead), exact in the products and sums of mma.m16n8k16.
-// One AND turns 32 bits of codes into two operand values, and only the sums over 32
-// values are multiplied by a scale.  The second sum is one more mma over the groups.
+// so the codes enter the matrix instructions (mma.m16n8k16) as they are: a 4-bit code in
+// the low bits of an fp16 word is the subnormal c 2^-24 (or 16 c 2^-24 from the next
+// nibble, with the query divided by 16 instead).  One AND turns 32 bits of codes into two
+// operand values, and only the sums over 32 values are multiplied by a scale.  The second
+// sum is one more mma over the groups.  (32-bit calls take one addition more, see low().)
 // Values the same way: O = sum_p w_p V_p = sum_g c (w s)_g + z_g w, the weights of a
 // position times its scale are the operand, and one mma holds the z part of all groups.
 // The softmax runs in one pass with a running maximum and sum per row; the operand w s
@@ -59,6 +59,33 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ uint32_t hsub1024(uint32_t a) {
+  const uint32_t k = 0xE400E400u;  // -1024, -1024
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Two codes of a word as operands, c and c' of one half each: their bits as they are, the
+// subnormals c 2^-24 (16 c 2^-24 from the second nibbles), or NORMAL numbers c (16 c).  The
+// matrix unit aligns products by the exponents of their operands, and a subnormal's is the
+// smallest normal one, so up to ten bits go where a code is small: enough bits are left for
+// 16-bit outputs, but not for 32-bit ones (8 lanes of about 1000 positions: 4e-5 off in the
+// 2-norm, one of 16384 1.2e-4).
+template <bool NORMAL>
+__device__ __forceinline__ uint32_t low(uint32_t x) {
+  return NORMAL ? hsub1024((x & 0x000F000Fu) | 0x64006400u) : x & 0x000F000Fu;
+}
+template <bool NORMAL>
+__device__ __forceinline__ uint32_t high(uint32_t x) {
+  return NORMAL ? hsub1024((x & 0x00F000F0u) | 0x64006400u) : x & 0x00F000F0u;
+}
+// Sums over many positions are kept out of the matrix unit in 32-bit calls: it cuts its
+// sums off instead of rounding them, and the codes' sums all grow in one direction (eight
+// lanes of about 1000 positions: 4e-5 off in the 2-norm with the sums kept there).
+__device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
+  const float2 x = __fadd2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+  const float2 y = __fadd2_rn(make_float2(a[2], a[3]), make_float2(b[2], b[3]));
+  a[0] = x.x; a[1] = x.y; a[2] = y.x; a[3] = y.y;
+}
 __device__ __forceinline__ uint4 lds_u4(const uint8_t* p) { return lds128(smem_u32(p)); }
 __device__ __forceinline__ uint32_t lds_u1(const uint8_t* p) { return lds32(smem_u32(p)); }
 __device__ __forceinline__ float ex2(float x) {
@@ -103,6 +130,11 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   using L = Kv4<D>;
   constexpr int G = L::G;
   constexpr bool kF32 = sizeof(T) == 4;
+  constexpr float kCode = kF32 ? 1.f : 16777216.f;  // a code's value over its operand's
+  // weight * scale as two fp16 parts, exactly: the codes' part of a value and the minimum's
+  // largely cancel, and then see the same weight.  (With one rounding more, fp16 outputs
+  // are 5.1e-4 off instead of their own rounding's 2.1e-4; bf16's is 1.7e-3.)
+  constexpr bool kExact = kF32 || std::is_same<T, __half>::value;
   constexpr int MT = kF32 ? NT : (NT + 1) / 2;          // 16-row operands of the queries
   constexpr int kTilesPerStage = kStageBytes / L::kBytes;
   constexpr int kStagePos = kTilesPerStage * kKv4Tile;  // positions of a stage
@@ -222,7 +254,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     const float up = __uint_as_float((uint32_t)(127 + max(e, -126)) << 23);
     const float signed_up = a.scale_log2 < 0.f ? -up : up;
     // (never zero: it multiplies the -inf of masked positions)
-    kscale[t] = fmaxf(fabsf(a.scale_log2) * 16777216.f / up, 1e-37f);
+    kscale[t] = fmaxf(fabsf(a.scale_log2) * kCode / up, 1e-37f);
     lim[t] = live ? start + r / a.rep + 1 : 0;
     float sums[G];
 #pragma unroll
@@ -328,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
         for (int n = 0; n < 2; ++n) {
           float c[4];
           mma16816_zero(c, qz[mt][0], qz[mt][1], qz[mt][2], qz[mt][3], kz[n], kz[n]);
-          const float2 unit = make_float2(3.814697265625e-6f, 3.814697265625e-6f);  // 2^(6 - 24)
+          const float2 unit = make_float2(64.f / kCode, 64.f / kCode);
           float2 acc0 = __fmul2_rn(make_float2(c[0], c[1]), unit), acc1;  // rows 0..7, 8..15
           if constexpr (!kF32 && NT > 1) acc1 = __fmul2_rn(make_float2(c[2], c[3]), unit);
 #pragma unroll
@@ -336,17 +368,17 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
             const uint32_t w = kc[n * G + g], w8 = w >> 8;
             const float2 sc = make_float2(h_lo(ks[n * G + g]), h_hi(ks[n * G + g]));
             float d[4];
-            mma16816_zero(d, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w & 0x000F000Fu,
-                          w & 0x00F000F0u);
+            mma16816_zero(d, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], low<kF32>(w),
+                          high<kF32>(w));
             float2 d0, d1;
             if constexpr (kBoth) {
               float e[4];
-              mma16816_zero(e, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], w8 & 0x000F000Fu,
-                            w8 & 0x00F000F0u);
+              mma16816_zero(e, qa[mt][g][0][0], qa[mt][g][0][1], qa[mt][g][0][2], qa[mt][g][0][3], low<kF32>(w8),
+                            high<kF32>(w8));
               d0 = __fadd2_rn(make_float2(d[0], d[1]), make_float2(e[2], e[3]));
             } else {
-              mma16816(d, qa[mt][g][1][0], qa[mt][g][1][1], qa[mt][g][1][2], qa[mt][g][1][3], w8 & 0x000F000Fu,
-                       w8 & 0x00F000F0u);
+              mma16816(d, qa[mt][g][1][0], qa[mt][g][1][1], qa[mt][g][1][2], qa[mt][g][1][3], low<kF32>(w8),
+                       high<kF32>(w8));
               d0 = make_float2(d[0], d[1]);
               d1 = make_float2(d[2], d[3]);
               if constexpr (kF32) d0 = __fadd2_rn(d0, d1);
@@ -450,8 +482,15 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
           if constexpr (kF32) split2(w[t][2 * n], w[t][2 * n + 1], wp[t][n], wl[t][n]);
           else wp[t][n] = pack_h(w[t][2 * n], w[t][2 * n + 1]);
         }
-        mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);  // (rows 8..15 are not used)
-        if constexpr (kF32) mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wl[t][0], wl[t][1]);
+        // (rows 8..15 are not used)
+        if constexpr (kF32) {
+          float z[4];
+          mma16816_zero(z, vz[0], vz[0], vz[1], vz[1], wl[t][0], wl[t][1]);
+          mma16816(z, vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);
+          add4(oz[t], z);
+        } else {
+          mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);
+        }
       }
       uint32_t vc[2 * G];
 #pragma unroll
@@ -462,8 +501,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint32_t x0 = vc[2 * g], x1 = vc[2 * g + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-        const uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
-        const uint32_t b0 = y0 & 0x000F000Fu, b1 = y0 & 0x00F000F0u, b2 = y1 & 0x000F000Fu, b3 = y1 & 0x00F000F0u;
+        const uint32_t a0 = low<kF32>(x0), a1 = high<kF32>(x0), a2 = low<kF32>(x1), a3 = high<kF32>(x1);
+        const uint32_t b0 = low<kF32>(y0), b1 = high<kF32>(y0), b2 = low<kF32>(y1), b3 = high<kF32>(y1);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           uint32_t p[2], q[2];
@@ -471,19 +510,30 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
           for (int n = 0; n < 2; ++n) {
             const uint32_t sc = vs[n * G + g];
             if constexpr (kF32) split2(w[t][2 * n] * h_lo(sc), w[t][2 * n + 1] * h_hi(sc), p[n], q[n]);
+            else if constexpr (kExact) split2(h_lo(wp[t][n]) * h_lo(sc), h_hi(wp[t][n]) * h_hi(sc), p[n], q[n]);
             else p[n] = hmul2(wp[t][n], sc);
             if constexpr (kMasked) {  // a scale behind the mask may be anything
               const int at = pos + 16 * u + 8 * n + 2 * tig;
               const uint32_t keep = (at < lim[t] && at < p1 ? 0xFFFFu : 0u) | (at + 1 < lim[t] && at + 1 < p1 ? 0xFFFF0000u : 0u);
               p[n] &= keep;
-              if constexpr (kF32) q[n] &= keep;
+              if constexpr (kExact) q[n] &= keep;
             }
           }
-          mma16816(o[t][g][0], a0, a1, a2, a3, p[0], p[1]);
-          mma16816(o[t][g][1], b0, b1, b2, b3, p[0], p[1]);
           if constexpr (kF32) {
-            mma16816(o[t][g][0], a0, a1, a2, a3, q[0], q[1]);
-            mma16816(o[t][g][1], b0, b1, b2, b3, q[0], q[1]);
+            float y0[4], y1[4];
+            mma16816_zero(y0, a0, a1, a2, a3, q[0], q[1]);
+            mma16816_zero(y1, b0, b1, b2, b3, q[0], q[1]);
+            mma16816(y0, a0, a1, a2, a3, p[0], p[1]);
+            mma16816(y1, b0, b1, b2, b3, p[0], p[1]);
+            add4(o[t][g][0], y0);
+            add4(o[t][g][1], y1);
+          } else {
+            mma16816(o[t][g][0], a0, a1, a2, a3, p[0], p[1]);
+            mma16816(o[t][g][1], b0, b1, b2, b3, p[0], p[1]);
+            if constexpr (kExact) {
+              mma16816(o[t][g][0], a0, a1, a2, a3, q[0], q[1]);
+              mma16816(o[t][g][1], b0, b1, b2, b3, q[0], q[1]);
+            }
           }
         }
       }
@@ -538,9 +588,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int j = 0; j < 2; ++j) {
         float* d0 = ob + (warp * kRows + 8 * t + 2 * tig) * D + 32 * g + 4 * gid + 2 * j;
         *reinterpret_cast<float2*>(d0) =
-            make_float2(fmaf(o[t][g][j][0], 16777216.f, z0), fmaf(o[t][g][j][2], 1048576.f, z0));
+            make_float2(fmaf(o[t][g][j][0], kCode, z0), fmaf(o[t][g][j][2], kCode / 16.f, z0));
         *reinterpret_cast<float2*>(d0 + D) =
-            make_float2(fmaf(o[t][g][j][1], 16777216.f, z1), fmaf(o[t][g][j][3], 1048576.f, z1));
+            make_float2(fmaf(o[t][g][j][1], kCode, z1), fmaf(o[t][g][j][3], kCode / 16.f, z1));
       }
     }
   }

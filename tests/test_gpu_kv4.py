@@ -575,3 +575,21 @@ def test_a_decoder_step_from_the_stand_alone_stages():
         n = want / torch.sqrt((want * want).mean(-1, keepdim=True) + 1e-5)
         assert (logits.double() - n @ f64[4].T).abs().max() < 1e-3
         x = y  # the next step sees another state
+
+
+@pytest.mark.parametrize("d,lens,new", [(64, [2000], [1]), (128, [900, 1500], [1, 1]), (64, [16384], [1]), (64, [600], [200])])
+def test_32_bit_calls_keep_32_bits(d, lens, new):
+    """The 2-norm of the error over that of the result.  Every part of the computation is good
+    to 2^-21 of its terms, and the terms' signs vary: 2^-18 leaves a factor of 8 for the
+    codes' and the minima's parts, which partly cancel.  Keys with large channels, as a
+    decoder makes them."""
+    s = Setup(d, 2, lens, new)
+    kv = s.fill()
+    q = s.rand(s.rows, 8, "fp32")
+    out = torch.empty_like(q)
+    s.cache.attend(0, q, out, s.batch)
+    got = out.double().cpu().numpy()
+    for i, (n_len, n) in enumerate(zip(lens, new)):
+        a, b = s.cu_np[i], s.cu_np[i + 1]
+        want, _ = R.attention(q[a:b].double().cpu().numpy(), *kv[i], n_len, R.default_scale(d))
+        assert np.linalg.norm(got[a:b] - want) / np.linalg.norm(want) < 2.0**-18
