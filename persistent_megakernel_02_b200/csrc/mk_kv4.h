@@ -26,12 +26,21 @@ struct Kv4Attn {
   float scale_log2;  // scale * log2(e)
 };
 
+// ... and how a call is split.  A row tile's rows of one split go to part as
+// [reference, sum of the weights, -, -, D sums], in fp32.
+struct Kv4AttnSplit : Kv4Attn {
+  int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page, of 128 for prompts)
+  int n_rt;                // row tiles
+  float* part;             // [seq][kv head][row tile, the last first][split][rows of a tile][D + 4]
+};
+
 // Opt-in to more than 48 KiB of shared memory (and to clusters of more than 8 CTAs), once
 // per kernel and device.
 bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready, bool large_cluster = false);
 
 // Attention of many query rows of 16-bit types (mk_kv4_prompt.cu).
-mk_status kv4_prompt(const Kv4Attn& a, int32_t dtype, cudaStream_t s);
+constexpr int kKv4PromptRows = 256;  // rows of its tiles
+mk_status kv4_prompt(const Kv4AttnSplit& a, int32_t dtype, cudaStream_t s);
 
 // Quantise (write) or read back positions start .. start + n - 1 of a slot of a handle's
 // cache [layer][physical page][kv head][K, V][PL][d], all layers; arguments checked by the caller.

@@ -17,8 +17,11 @@
 // Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
 // A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
-// merged.  Splits along the positions, where rows are few, are joined by a second
-// small kernel.
+// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 148 us, 4.8 TB/s,
+// 0.73 of the copy rate; the copies alone take 117, the instructions alone 144 (64-value
+// heads: 24 sequences 57 us for 32 of bytes).  Fewer registers for a fifth CTA on the SM
+// spill and lose (267 us).  Splits along the positions, where rows are few, are joined in
+// the cluster's shared memory or by a second small kernel.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -39,11 +42,7 @@ constexpr int kStageBytes = 5120;
 constexpr int kStages = 2;  // ring depth per warp
 constexpr int kHead = 4;    // log2 of what a weight may pass the reference by
 
-struct AttnArgs : Kv4Attn {
-  int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page)
-  int n_rt;                // row tiles
-  float* part;             // [seq][kv head][row tile][split][8 NT][D + 4]
-};
+using AttnArgs = Kv4AttnSplit;
 
 // c += A B (16 x 16 by 16 x 8), and the same from zero
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -657,9 +656,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 
 // Joins the splits of a row, a CTA per row: a warp's lanes look at the splits' references
 // and sums together, then D / 4 threads per split sum the values, all loads independent.
-template <int D, class T, int NT>
+template <int D, class T, int ROWS>
 __global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
-  constexpr int kRows = 8 * NT, kPer = D / 4, kGroups = 128 / kPer;
+  constexpr int kRows = ROWS, kPer = D / 4, kGroups = 128 / kPer;
   __shared__ float4 red[kGroups][kPer];
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.x % kRows, tile = blockIdx.x / kRows;
@@ -714,8 +713,45 @@ __global__ void __launch_bounds__(128) attn_join(const AttnArgs a) {
   store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * threadIdx.x * sizeof(T), y);
 }
 
+// The same for a prompt's tiles, many rows of few splits: D / 8 threads per row, one split
+// after another (a CTA per row took 16 us for 64 tiles of 256 rows).
+template <int D, class T>
+__global__ void __launch_bounds__(128) attn_join_prompt(const AttnArgs a) {
+  constexpr int kRows = kKv4PromptRows, kPer = D / 8, kStep = 128 / kPer, kCtas = kRows / kStep;
+  const int w8 = threadIdx.x % kPer, r = blockIdx.x % kCtas * kStep + threadIdx.x / kPer, tile = blockIdx.x / kCtas;
+  int idx = tile;
+  const int rt = a.n_rt - 1 - idx % a.n_rt;
+  idx /= a.n_rt;
+  const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
+  const Kv4Seq seq = kv4_seq(a.b, si);
+  const int n_rows = seq.n * a.rep, row0 = rt * kRows, last_row = min(n_rows, row0 + kRows) - 1, row = row0 + r;
+  const int see_any = max(0, seq.len - seq.n + last_row / a.rep + 1);
+  const int n = max(1, min(a.n_split, (see_any + a.split_len - 1) / a.split_len));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!seq.ok || row > last_row) return;
+  const float* part = a.part + ((size_t)tile * a.n_split * kRows + r) * (D + 4);
+  const size_t stride = (size_t)kRows * (D + 4);
+  float top = -INFINITY, sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) top = fmaxf(top, __ldcg(part + s * stride));
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float* p = part + s * stride;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p + 4 + 8 * w8)), v = __ldcg(reinterpret_cast<const float4*>(p + 8 + 8 * w8));
+    const float f = top == -INFINITY ? 0.f : ex2(ml.x - top), y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    sum = fmaf(f, ml.y, sum);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(f, y[i], x[i]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= inv;
+  store8<T>(a.out + (seq.row0 + row / a.rep) * a.o_row + (head * a.rep + row % a.rep) * a.o_head + 8 * w8 * sizeof(T), x);
+}
+
 struct Plan {
-  bool prompt;  // many rows of 16-bit queries: the tcgen05 kernel, unsplit
+  bool prompt;  // many rows of 16-bit queries: the tcgen05 kernel
   int nt, n_rt, n_split, split_len;
   bool cluster;  // the splits of a row tile are a cluster and join in shared memory
   long long ctas;
@@ -738,17 +774,40 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   const int sms = sm_count();
   if (sms <= 0) return MK_ERR_CUDA;
   const long long rows = std::max<long long>(b->max_new, 1) * rep;  // 0: still looks at the spans
-  p->prompt = dtype != 2 && rows >= 128;
-  if (p->prompt) {
-    p->n_split = 1;
-    p->cluster = false;
-    p->part_bytes = 0;
-    return MK_OK;
+  // Many rows of 16-bit types: 256-row tiles on tcgen05, where that is expected to be
+  // faster.  Measured (one B200, us, 64- / 128-value heads): there a tile of 128 positions takes
+  // 1.85 / 2.2 and a CTA 6 more, one CTA on an SM, and a join 5 and 0.35 per split; here
+  // 16 rows x 16 positions take 0.00033 / 0.00062 of the whole GPU, and a call 10 more.  E.g.
+  // 8 kv heads x 4 query heads over 16384 positions, 64 values: 16 new tokens 24 here, 27
+  // there; 128 tokens 106 here, 243 there unsplit, 45 split; 512 tokens 334, 248, 134.
+  const long long seq_heads = (long long)b->n_seqs * c->n_kv_heads;
+  p->prompt = false;
+  if (dtype != 2 && rows > 16) {
+    const bool wide = c->head_dim == 128;
+    const long long n_blocks = (rows + kKv4PromptRows - 1) / kKv4PromptRows, base = n_blocks * seq_heads;
+    const long long tiles = (b->max_len + 127) / 128;
+    // splits of at least four tiles, as many as keep one CTA per SM
+    const long long n_split = std::max(1ll, std::min(sms / std::max(base, 1ll), tiles / 4));
+    const long long per = std::max(1ll, (tiles + n_split - 1) / n_split);
+    const double here = 10 + (double)seq_heads * ((rows + 15) / 16) * ((b->max_len + 15) / 16) * (wide ? 0.00062 : 0.00033);
+    const double there = (double)((base * n_split + sms - 1) / sms) * (6 + per * (wide ? 2.2 : 1.85)) + (n_split > 1 ? 5 + 0.35 * n_split : 0);
+    if (there < here) {
+      p->prompt = true;
+      p->cluster = false;
+      p->nt = 0;
+      p->n_rt = (int)n_blocks;
+      p->n_split = (int)((tiles + per - 1) / std::max(per, 1ll));
+      if (p->n_split < 1) p->n_split = 1;
+      p->split_len = (int)std::min<long long>(per * 128, 0x7FFFFF80);
+      p->ctas = base * p->n_split;
+      if (p->ctas > 0x7FFFFFFF / kKv4PromptRows) return MK_ERR_UNSUPPORTED;
+      p->part_bytes = p->n_split > 1 ? p->ctas * kKv4PromptRows * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
+      return MK_OK;
+    }
   }
-  const int most = c->head_dim == 64 && dtype != 2 ? 4 : 2;
-  p->nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
+  p->nt = rows <= 8 ? 1 : 2;
   const long long n_rt = (rows + 8 * p->nt - 1) / (8 * p->nt);
-  const long long base = (long long)b->n_seqs * c->n_kv_heads * n_rt;
+  const long long base = seq_heads * n_rt;
   const int unit = MK_KV4_PAGE;
   const long long pages = (b->max_len + unit - 1) / unit;
   // Splits: enough that every SM has about two CTAs, in pieces of at least a page per warp
@@ -780,6 +839,25 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   return MK_OK;
 }
 
+// A join, launched while the splits run (its first loads wait for them).
+template <int D, class T, int ROWS>
+mk_status launch_join(const AttnArgs& a, const Plan& p, cudaStream_t s) {
+  constexpr bool kPrompt = ROWS == kKv4PromptRows;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  cfg.gridDim = dim3((unsigned)(p.ctas / p.n_split * (kPrompt ? ROWS / (128 / (D / 8)) : ROWS)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if constexpr (kPrompt) e = cudaLaunchKernelEx(&cfg, attn_join_prompt<D, T>, a);
+  else e = cudaLaunchKernelEx(&cfg, attn_join<D, T, ROWS>, a);
+  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
 template <int D, class T, int NT>
 mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   constexpr int kMerge = 8 * NT * (kWarps * (D + 2) + D + 4) * 4;
@@ -803,26 +881,13 @@ mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   }
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT, false>), kSmem, &ready, false)) return MK_ERR_CUDA;
   if (cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, false>, a) != cudaSuccess) return MK_ERR_CUDA;
-  if (p.n_split > 1) {
-    // launched while the splits run (its first loads wait for them)
-    cfg.gridDim = dim3((unsigned)(p.ctas / p.n_split * 8 * NT));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, attn_join<D, T, NT>, a) != cudaSuccess) return MK_ERR_CUDA;
-  }
-  return MK_OK;
+  return p.n_split > 1 ? launch_join<D, T, 8 * NT>(a, p, s) : MK_OK;
 }
 
 template <int D, class T>
 mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   if (p.nt == 1) return launch_few<D, T, 1>(a, p, s);
-  if (p.nt == 2) return launch_few<D, T, 2>(a, p, s);
-  if constexpr (D == 64 && sizeof(T) == 2) return launch_few<D, T, 4>(a, p, s);
-  return MK_ERR_UNSUPPORTED;
+  return launch_few<D, T, 2>(a, p, s);
 }
 
 mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, int32_t n_heads, int32_t dtype) {
@@ -882,12 +947,20 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
   if (p.part_bytes > 0 && (!workspace || ((uintptr_t)workspace & 15u) || workspace_bytes < p.part_bytes))
     return MK_ERR_INVALID_ARG;
   const int size = dtype == 2 ? 4 : 2;
-  AttnArgs a{{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p), q->row_stride * size,
+  const AttnArgs a{{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p), q->row_stride * size,
               q->head_stride * size, out->row_stride * size, out->head_stride * size, layer, rep,
               scale * 1.44269504088896341f},
              p.n_split, p.split_len, p.n_rt, static_cast<float*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.prompt) return kv4_prompt(a, dtype, s);
+  if (p.prompt) {
+    st = kv4_prompt(a, dtype, s);
+    if (st != MK_OK || p.n_split == 1) return st;
+    if (cache->head_dim == 64)
+      return dtype == 0 ? launch_join<64, __nv_bfloat16, kKv4PromptRows>(a, p, s)
+                        : launch_join<64, __half, kKv4PromptRows>(a, p, s);
+    return dtype == 0 ? launch_join<128, __nv_bfloat16, kKv4PromptRows>(a, p, s)
+                      : launch_join<128, __half, kKv4PromptRows>(a, p, s);
+  }
   if (cache->head_dim == 64) {
     if (dtype == 0) return launch_few<64, __nv_bfloat16>(a, p, s);
     if (dtype == 1) return launch_few<64, __half>(a, p, s);

@@ -6,19 +6,25 @@
 //   warps 0-3, 4-7  softmax of query tile 0, 1: one thread per row
 //   warps 8-11      dequantise: codes to fp16 K and V in the swizzled shared-memory layout
 //   warps 12, 13    issue the matrix instructions of query tile 0, 1
-// Per tile: S = Q K^T into tensor memory (128 x 128 fp32); the row's thread reads S twice
-// (maximum, then weights) and writes the weights back over S as fp16, from where they are
-// the A operand of O += W V, which stays in tensor memory.  The two query tiles alternate:
-// while one is in its softmax, the tensor cores work for the other.
+// Scores S = Q K^T of a half tile (64 positions) go into 64 columns of tensor memory; the
+// row's thread reads them once (maximum, weights) and writes the weights over them as fp16,
+// from where they are the A operand of O += W V, which stays in tensor memory.  The next
+// half's scores are under way meanwhile, K's buffers are freed apart from V's, and each
+// query tile has an issuing warp of its own, so that neither waits for the other.
 //
-// K and V are z + s c rounded once to fp16 (one HFMA2 for two values), queries are scaled
+// K and V are z + s c rounded once to fp16 (2^-12: 16-bit types only), queries are scaled
 // by a power of two per row, which is exact in fp16 but for values 2^-24 below the row's
-// largest.  The order of values inside 8 and of positions inside 32 is the one the codes
-// come in: queries are permuted alike, and S, W and V share the order of positions.
-// O is rescaled only when a score passes the row's reference by more than 16x.
+// largest, weights are rounded to fp16.  The order of values inside 8 and of positions
+// inside 32 is the one the codes come in: queries are permuted alike, and S, W and V
+// share the order of positions.  O is rescaled only when a score passes the row's
+// reference by more than 16x.
 //
-// Bound: one exponential per score and the two products; 128 x 128 x D scores cost the
-// tensor cores 128 D / 32 cycles... see the figures at the launch.
+// Bound: with 64-value heads the exponentials, 16 per SM and cycle: 2048 cycles for the
+// 256 x 128 scores of a tile, 1024 for its products.  A tile takes about 3500 (1.85 us), the
+// warps' instructions in between: 2048 tokens x 32 heads over 8192 positions 217 us, 550
+// TFLOP/s; 2048 tokens of 128-value heads, causal, 55 us, 620 TFLOP/s.  (Three or four
+// query tiles, which would fill the exponential unit, do not fit tensor memory; sixteen
+// softmax warps for the two, 32 columns each, measured 267 us for the former.)
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -170,7 +176,7 @@ __host__ __device__ constexpr int column_position(int c) {
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int n_blocks) {
+__global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a) {
   using L = Kv4<D>;
   constexpr int G = L::G;
   constexpr uint32_t kIdQK = idesc_f16(128, 64), kIdWV = idesc_f16(128, D);
@@ -182,7 +188,9 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   int idx = blockIdx.x;
-  const int blk = n_blocks - 1 - idx / (a.c.n_kv_heads * a.b.n_seqs);  // the blocks that see most come first
+  const int split = idx % a.n_split;
+  idx /= a.n_split;
+  const int blk = a.n_rt - 1 - idx / (a.c.n_kv_heads * a.b.n_seqs);  // the blocks that see most come first
   idx %= a.c.n_kv_heads * a.b.n_seqs;
   const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
   const Kv4Seq seq = kv4_seq(a.b, si);
@@ -193,13 +201,15 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
   const int n_rows = seq.n * a.rep, row0 = blk * 2 * kPTile;
   if (row0 >= n_rows) return;
   const int start = seq.len - seq.n;  // position of the first query token (may be negative)
-  int n_half[2], n_max = 0;           // halves of 64 positions each query tile sees; tiles of 128
+  const int p0 = split * a.split_len;  // this split's positions: p0 .. p0 + split_len - 1
+  int n_half[2], n_max = 0;            // halves of 64 positions each query tile sees of them; tiles of 128
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int first = row0 + t * kPTile, last = min(n_rows, first + kPTile) - 1;
-    n_half[t] = first < n_rows ? (max(0, start + last / a.rep + 1) + 63) / 64 : 0;
+    n_half[t] = first < n_rows ? (max(0, min(start + last / a.rep + 1 - p0, a.split_len)) + 63) / 64 : 0;
     n_max = max(n_max, (n_half[t] + 1) / 2);
   }
+  if (n_max == 0 && split > 0) return;  // the join takes only the splits that hold something
 
   if (tid < 4) sh.nan_first[tid] = 0x7FFFFFFF;
   if (tid == 0) {
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
       tc_fence_after();
       uint32_t s[64];
       tmem_get64(ts + 64 * h, s);
-      const int base = i * 64, left = lim - base;  // columns with position < left are seen
+      const int base = p0 + i * 64, left = lim - base;  // columns with position < left are seen
       const uint32_t bad0 = sh.bad[buf][2 * h], bad1 = sh.bad[buf][2 * h + 1];
       float mx;
       if (whole && base + 64 <= lim_warp && (bad0 | bad1) == 0) {
@@ -348,7 +358,11 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     if (n > 0 && ok) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.o_full[t], 0, a.c.status));
     if (ok) {
       tc_fence_after();
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // 0: the row sees nothing
+      // splits are joined later: the sums as they are, after the reference and the weights' sum
+      const float inv = sum == 0.f ? 0.f : a.n_split > 1 ? 1.0f : 1.0f / sum;  // 0: the row sees nothing
+      const size_t tile = (size_t)(si * a.c.n_kv_heads + head) * a.n_rt + (a.n_rt - 1 - blk);
+      float* part = a.part + ((tile * a.n_split + split) * (2 * kPTile) + t * kPTile + r_in) * (D + 4);
+      if (a.n_split > 1 && live) *reinterpret_cast<float2*>(part) = make_float2(sum == 0.f ? -INFINITY : ref, sum);
       char* dst = a.out + (long long)(seq.row0 + row / a.rep) * a.o_row +
                   (long long)(head * a.rep + row % a.rep) * a.o_head;
 #pragma unroll
@@ -364,7 +378,9 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
             x[i] = n > 0 && sum != 0.f ? __uint_as_float(o[8 * hh + i]) * inv : 0.f;
             if (nan) x[i] = __uint_as_float(0x7FFFFFFFu);
           }
-          if (live) store8<T>(dst + (c0 + 8 * hh) * sizeof(T), x);
+          if (!live) continue;
+          if (a.n_split > 1) store8<float>(part + 4 + c0 + 8 * hh, x);
+          else store8<T>(dst + (c0 + 8 * hh) * sizeof(T), x);
         }
       }
     }
@@ -372,14 +388,14 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     // ---------------- dequantise: warp 8 + w has positions 32 w .. 32 w + 31 of a tile ----------------
     const int w = warp - 8, gid = lane >> 2, tig = lane & 3;
     const int32_t* table = a.b.block_table + (size_t)si * a.b.max_pages;
-    const int see = min(seq.len, n_max * kPTile);  // positions behind are left out (zero)
+    const int see = min(seq.len, p0 + n_max * kPTile);  // positions behind are left out (zero)
     // raw operands of this warp's two 16-position tiles
     uint4 kc[2][2 * G / 4] = {}, vc[2][2 * G / 4] = {}, vs[2][2 * G / 4] = {}, ks[2][2] = {};
     uint2 kz[2][2] = {};
     uint32_t vz[2][G][2] = {};
     // page id of tile j, looked up a tile ahead of its loads; -2: no position there
     auto look = [&](int j) {
-      const int p = j * kPTile + 32 * w;
+      const int p = p0 + j * kPTile + 32 * w;
       return j < n_max && p < see ? table[p / MK_KV4_PAGE] : -2;
     };
     auto tile_at = [&](int page) {
@@ -457,8 +473,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
     };
     // V of tile j transposed: row of value 32 g + 4 gid + i, 8 positions (16 bytes) per lane
     auto put_v = [&](int j, int page) {
-      const int buf = j & 1, p0 = j * kPTile + 32 * w;
-      const int left = (unsigned)page < (unsigned)a.c.n_pages ? see - p0 : 0;  // positions of the block that exist
+      const int buf = j & 1, first = p0 + j * kPTile + 32 * w;
+      const int left = (unsigned)page < (unsigned)a.c.n_pages ? see - first : 0;  // positions of the block that exist
       uint32_t odd = 0;  // a NaN among the parameters
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -485,7 +501,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               const uint32_t z = vz[u][g][n];
-              const int p = p0 + 16 * u + 8 * n + 2 * tig;
+              const int p = first + 16 * u + 8 * n + 2 * tig;
               if (nan_half(z) || nan_half(z >> 16)) atomicMin(&sh.nan_first[g], nan_half(z) ? p : p + 1);
               const uint32_t keep = (nan_half(z) ? 0u : 0xFFFFu) | (nan_half(z >> 16) ? 0u : 0xFFFF0000u);
               vz[u][g][n] &= keep;
@@ -604,17 +620,16 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4Attn a, int
 }  // namespace
 
 template <int D, class T>
-static mk_status launch(const Kv4Attn& a, cudaStream_t s) {
+static mk_status launch(const Kv4AttnSplit& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_prompt<D, T>), PSmem<D>::kBytes, &ready)) return MK_ERR_CUDA;
-  const long long n_blocks = ((long long)a.b.max_new * a.rep + 2 * kPTile - 1) / (2 * kPTile);
-  const long long ctas = n_blocks * a.c.n_kv_heads * a.b.n_seqs;
+  const long long ctas = (long long)a.n_rt * a.c.n_kv_heads * a.b.n_seqs * a.n_split;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
-  attn_prompt<D, T><<<(unsigned)ctas, kPThreads, PSmem<D>::kBytes, s>>>(a, (int)n_blocks);
+  attn_prompt<D, T><<<(unsigned)ctas, kPThreads, PSmem<D>::kBytes, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
-mk_status kv4_prompt(const Kv4Attn& a, int32_t dtype, cudaStream_t s) {
+mk_status kv4_prompt(const Kv4AttnSplit& a, int32_t dtype, cudaStream_t s) {
   if (a.c.head_dim == 64) return dtype == 0 ? launch<64, __nv_bfloat16>(a, s) : launch<64, __half>(a, s);
   return dtype == 0 ? launch<128, __nv_bfloat16>(a, s) : launch<128, __half>(a, s);
 }

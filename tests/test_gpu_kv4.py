@@ -72,16 +72,33 @@ class Setup:
         return self.table_np[i, : -(-self.lens[i] // R.PAGE)]
 
 
+def reference(s, kv, q, i, scale):
+    """(out, reach) of sequence i (see _kv4.attention), in 64 bits on the GPU a kv head at a time."""
+    n_len, n = s.lens[i], s.new[i]
+    a, b = s.cu_np[i], s.cu_np[i + 1]
+    k, v = (torch.from_numpy(x).cuda() for x in kv[i])
+    heads, rep = q.shape[1], q.shape[1] // s.kv_heads
+    out = torch.zeros((n, heads, s.d), dtype=torch.float64, device="cuda")
+    reach = torch.zeros((n, heads), dtype=torch.float64, device="cuda")
+    see = torch.arange(n_len, device="cuda")[None, :] <= torch.arange(n_len - n, n_len, device="cuda")[:, None]
+    some = see.any(-1)
+    for h in range(heads if n_len and n else 0):
+        x, kk, vv = q[a:b, h].double(), k[:, h // rep], v[:, h // rep]
+        sc = (x @ kk.T * scale).masked_fill(~see, -np.inf)
+        out[some, h] = torch.softmax(sc[some], -1) @ vv
+        reach[:, h] = (x.abs() @ kk.abs().T * abs(scale)).masked_fill(~see, 0).amax(-1)
+    return out.cpu().numpy(), reach.cpu().numpy()
+
+
 def check_attention(s, kv, q, out, dtype, scale=None):
     scale = R.default_scale(s.d) if scale is None else scale
-    qn, on = q.double().cpu().numpy(), out.double().cpu().numpy()
+    on = out.double().cpu().numpy()
     for i, (n_len, n) in enumerate(zip(s.lens, s.new)):
         a, b = s.cu_np[i], s.cu_np[i + 1]
         if a == b:
             continue
-        k, v = kv[i]
-        want, reach = R.attention(qn[a:b], k, v, n_len, scale)
-        v_max = np.abs(v).max() if n_len else 0.0
+        want, reach = reference(s, kv, q, i, scale)
+        v_max = np.abs(kv[i][1]).max() if n_len else 0.0
         err = np.abs(on[a:b] - want)
         tol = R.tolerance(want, reach, v_max, dtype)
         assert np.isfinite(on[a:b]).all(), f"sequence {i}"
@@ -269,12 +286,112 @@ def test_nan_in_the_cache_reaches_only_the_rows_that_see_it(dtype, new):
     assert not out[:, 4:].isnan().any()
 
 
-def test_attention_with_other_strides():
-    s = Setup(128, 2, [90, 300], [40, 1], layers=2)
+# Enough rows for the tensor-memory kernel (16-bit types): whole and ragged blocks of 256 rows,
+# rows that end inside a tile of 128, spans longer than their sequence, single tokens beside
+# prompts, and few blocks over a long cache, which are split along it.
+MANY = [([1000, 777, 130], [1000, 700, 129], 8, 4), ([513, 64, 1, 0, 300, 256, 128, 65], [513, 64, 1, 0, 299, 200, 128, 33], 8, 4),
+        ([70, 400, 500, 380, 41, 450], [90, 380, 390, 1, 400, 2], 8, 4), ([6000], [600], 2, 4), ([5000, 3100], [333, 128], 1, 8),
+        ([700] * 5, [430] * 5, 8, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,kv_heads,rep", MANY)
+def test_attention_of_many_rows(lens, new, kv_heads, rep, d, dtype):
+    s = Setup(d, kv_heads, lens, new, pad_rows=2)
+    kv = s.fill()
+    q = s.rand(s.rows, kv_heads * rep, dtype)
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, out, s.batch)
+    s.cache.check()
+    check_attention(s, kv, q, out, dtype)
+    assert (out[s.cu_np[-1]:] == -7.0).all()
+    again = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, again, s.batch)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_attention_of_many_rows_scales(scale):
+    s = Setup(64, 8, [500] * 4, [400] * 4)
+    kv = s.fill(keys=0.2)
+    q = s.rand(s.rows, 32, "bf16")
+    out = torch.empty_like(q)
+    s.cache.attend(0, q, out, s.batch, scale=scale)
+    check_attention(s, kv, q, out, "bf16", scale)
+
+
+@pytest.mark.parametrize("k_size,q_size,v_size", [(2.0**-9, 2.0**7, 2.0**-7), (2.0**9, 2.0**-11, 2.0**9), (30.0, 1.0, 1.0)])
+def test_attention_of_many_rows_small_and_large_values(k_size, q_size, v_size):
+    s = Setup(128, 8, [420] * 3, [400] * 3)
+    b = s.full_batch()
+    k, v = s.rand(b.n_rows, 8, spread=k_size), s.rand(b.n_rows, 8, spread=v_size)
+    s.cache.append(0, k, v, b)
+    kv = [tuple(R.quantised(x[420 * i:420 * (i + 1)].double().cpu().numpy()) for x in (k, v)) for i in range(3)]
+    q = s.rand(s.rows, 32, "fp16", spread=q_size)
+    out = torch.empty_like(q)
+    s.cache.attend(0, q, out, s.batch)
+    check_attention(s, kv, q, out, "fp16")
+
+
+@pytest.mark.parametrize("lens,new", [([500] * 4, [300] * 4), ([6000], [600])])
+@pytest.mark.parametrize("where", ["keys", "values"])
+def test_nan_in_a_prompt_reaches_only_the_rows_that_see_it(where, lens, new):
+    """One position's K or V of kv head 0 is NaN in one group: later rows see it (all values for K,
+    the group's for V), earlier ones and the other heads do not."""
+    kvh = 8 if len(lens) > 1 else 2
+    s = Setup(64, kvh, lens, new)
+    s.fill()
+    q = s.rand(s.rows, 4 * kvh, "bf16")
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    s.cache.attend(0, q, clean, s.batch)
+    at = lens[0] - 77
+    one = s.cache.batch(torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                        torch.tensor([at + 1], dtype=torch.int32, device="cuda"), 1, 1, at + 1)
+    k, v = torch.empty((1, kvh, 64), device="cuda"), torch.empty((1, kvh, 64), device="cuda")
+    s.cache.read(0, k, v, one)
+    (k if where == "keys" else v)[0, 0, 40] = float("nan")
+    s.cache.append(0, k, v, one)
+    s.cache.attend(0, q, out, s.batch)
+    first, end = at - (lens[0] - new[0]), new[0]
+    bad = out[first:end, :4]
+    assert bad.isnan().all() if where == "keys" else bad[..., 32:].isnan().all() and not bad[..., :32].isnan().any()
+    assert torch.equal(out[:first], clean[:first]) and not out[:, 4:].isnan().any() and not out[end:].isnan().any()
+
+
+def test_missing_pages_of_a_prompt_are_reported_and_masked():
+    from persistent_megakernel_02_b200 import MkError
+
+    s = Setup(64, 8, [500] * 4, [300] * 4)
+    kv = s.fill()
+    q = s.rand(s.rows, 32, "bf16")
+    out = torch.empty_like(q)
+    for page in (s.cache.n_pages, -1):
+        s.table[1, 2] = page
+        s.cache.attend(0, q, out, s.batch)
+        with pytest.raises(MkError, match="DEVICE_FAULT"):
+            s.cache.check()
+        assert torch.isfinite(out).all()
+    cu = s.cu_np
+    for i in (0, 2, 3):  # the other sequences
+        want, reach = reference(s, kv, q, i, R.default_scale(64))
+        err = np.abs(out[cu[i]:cu[i + 1]].double().cpu().numpy() - want)
+        assert (err <= R.tolerance(want, reach, np.abs(kv[i][1]).max(), "bf16")).all()
+    k, v = (np.delete(x, slice(128, 192), 0) for x in kv[1])  # the rows behind it: as if it were not there
+    x = q[cu[2] - 100:cu[2]]
+    t = Setup(64, 8, [436], [100])
+    want, reach = reference(t, [(k, v)], x, 0, R.default_scale(64))
+    err = np.abs(out[cu[2] - 100:cu[2]].double().cpu().numpy() - want)
+    assert (err <= R.tolerance(want, reach, np.abs(v).max(), "bf16")).all()
+
+
+@pytest.mark.parametrize("kv_heads,lens,new", [(2, [90, 300], [40, 1]), (8, [500] * 4, [300] * 4)])
+def test_attention_with_other_strides(kv_heads, lens, new):
+    s = Setup(128, kv_heads, lens, new, layers=2)
     kv = s.fill(layer=1)
-    whole = s.rand(s.rows, 12, "fp16")
-    q = whole[:, 2:10]
-    out = torch.full((8, s.rows, 128), -1.0, dtype=torch.float16, device="cuda").transpose(0, 1)
+    whole = s.rand(s.rows, 4 * kv_heads + 4, "fp16")
+    q = whole[:, 2:-2]
+    out = torch.full((4 * kv_heads, s.rows, 128), -1.0, dtype=torch.float16, device="cuda").transpose(0, 1)
     s.cache.attend(1, q, out, s.batch)
     check_attention(s, kv, q, out, "fp16")
 
