@@ -358,8 +358,9 @@ mk_status mk_matvec_engine_status(void* stream);
  * their bounds.  A batch with numbers outside these bounds (cu not ascending from 0 to
  * at most n_rows, a span above max_new, a length below 0 or above max_len) or a page
  * id outside the pool is recorded in the cache's status word; the sequence or page it
- * concerns is neither written nor read.  Calls that overlap on the GPU must not
- * write the same positions, nor read what another writes. */
+ * concerns is neither written nor read.  Sequences may share pages that are only
+ * read; calls that overlap on the GPU, and the sequences of one call, must not write
+ * the same positions, nor may a call read what another writes meanwhile. */
 #define MK_KV4_PAGE 64
 
 typedef struct {
@@ -400,7 +401,7 @@ mk_status mk_kv4_append(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_b
 mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
                       const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream);
 
-/* Causal attention of the batch's query rows over the cache:
+/* Causal attention of the batch's query rows over the cache (max_new at most 2^27):
  *   out[r][h] = sum_p softmax_p(scale * q[r][h] . K[p][h / rep]) V[p][h / rep],
  * p over positions 0 .. kv_lens[i] - (cu[i+1] - cu[i]) + j of row j of sequence i,
  * rep = n_heads / n_kv_heads in {1, 2, 4, 8}.  A row that sees no position (its

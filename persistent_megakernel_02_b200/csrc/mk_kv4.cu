@@ -21,16 +21,21 @@ struct SlotRows {  // a handle's paged cache
   int n_phys_pages, PL;
 };
 
+// Row 0 of a tile and the distance to the next, of K or V (`which`) of a kv head: the tile's
+// rows are evenly spaced in both (a handle's page holds 32 or 64 positions, so a tile never
+// crosses one).  (Indexing by `which` would put the block in local memory.)
 template <int D, class T>
-__device__ __forceinline__ char* row_ptr(const BatchRows& b, int which, int, int row, int, int head, int) {
-  // (indexing by `which` would put the block in local memory)
-  return const_cast<char*>(which ? b.base[1] : b.base[0]) + row * (which ? b.row[1] : b.row[0]) +
-         head * (which ? b.head[1] : b.head[0]);
+__device__ __forceinline__ char* tile_rows(const BatchRows& b, int which, int, int row0, int, int head, int,
+                                           long long* step) {
+  *step = which ? b.row[1] : b.row[0];
+  return const_cast<char*>(which ? b.base[1] : b.base[0]) + row0 * *step + head * (which ? b.head[1] : b.head[0]);
 }
 template <int D, class T>
-__device__ __forceinline__ char* row_ptr(const SlotRows& s, int which, int layer, int, int pos, int head, int heads) {
-  const long long page = (long long)layer * s.n_phys_pages + s.table[pos / s.PL];
-  return s.kv + (((page * heads + head) * 2 + which) * s.PL + pos % s.PL) * (long long)(D * sizeof(T));
+__device__ __forceinline__ char* tile_rows(const SlotRows& s, int which, int layer, int, int pos0, int head, int heads,
+                                           long long* step) {
+  const long long page = (long long)layer * s.n_phys_pages + s.table[pos0 / s.PL];
+  *step = D * (long long)sizeof(T);
+  return s.kv + (((page * heads + head) * 2 + which) * s.PL + pos0 % s.PL) * *step;
 }
 
 // What a warp works on: one tile of one sequence and kv head.
@@ -93,14 +98,15 @@ __device__ __forceinline__ void quantise_tile(const mk_kv4_cache& c, const TileJ
   // 16-byte stores: codes of K or of V, 8 D bytes, then scales and minima, 2 D bytes.
   // Part of a tile (a new token) goes out value by value; the other rows stay as they are.
   auto load = [&](Raw8<T> (&raw)[4], int b0) {  // accesses b0 .. b0 + 3: K has 0 .. kItems - 1, V the next
-    const int which = b0 >= kItems;
+    const int which = b0 >= kItems, r0 = (b0 - which * kItems) * kStep + rl;
+    long long step;
+    const char* p = tile_rows<D, T>(rows, which, j.layer, j.row0 - skip, j.tile * kKv4Tile, head, c.n_kv_heads, &step) +
+                    r0 * step + w * 8 * sizeof(T);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (b0 - which * kItems + i) * kStep + rl;
+    for (int i = 0; i < 4; ++i, p += kStep * step) {
+      const int r = r0 + i * kStep;
       raw[i] = Raw8<T>{};
-      if (r >= skip && r < stop)
-        raw[i] = load_raw8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head,
-                                            c.n_kv_heads) + w * 8 * sizeof(T));
+      if (r >= skip && r < stop) raw[i] = load_raw8<T>(p);
     }
   };
   Raw8<T> next[4];
@@ -192,11 +198,14 @@ __device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& 
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     if (kReadParts<T> == 2 && which != part_of) continue;
+    long long step;
+    char* p = tile_rows<D, T>(rows, which, j.layer, j.row0 - skip, j.tile * kKv4Tile, head, c.n_kv_heads, &step) +
+              rl * step + w * 8 * sizeof(T);
     const uint8_t* codes_at = image + (which ? L::v_unit(rl, 2 * w) : L::k_word(rl, w));
     const uint8_t* scale_at = image + (which ? L::kVs : L::kKs) + L::scale(rl, w / 4);
     const uint8_t* min_at = image + (which ? L::v_min(rl, w / 4) : L::k_min(rl, w / 4));
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
+    for (int i = 0; i < kItems; ++i, p += kStep * step) {
       const int r = i * kStep + rl;
       uint32_t codes;
       if (which == 0) {
@@ -212,9 +221,7 @@ __device__ __forceinline__ void read_tile(const mk_kv4_cache& c, const TileJob& 
               min_at + (which ? L::v_min(i * kStep, 0) - L::kVz : L::k_min(i * kStep, 0) - L::kKz)) << 16;
       float x[8];
       kv4_values(codes, h_lo(params), h_hi(params), x);
-      if (r >= skip && r < stop)
-        store8<T>(row_ptr<D, T>(rows, which, j.layer, j.row0 + r - skip, j.tile * kKv4Tile + r, head, c.n_kv_heads) +
-                      w * 8 * sizeof(T), x);
+      if (r >= skip && r < stop) store8<T>(p, x);
     }
   }
 }
@@ -316,7 +323,7 @@ mk_status kv4_check(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b,
   if (b->n_seqs < 1 || b->max_pages < 1 || b->n_rows < 0 || b->max_new < 0 || b->max_len < 0) return MK_ERR_INVALID_ARG;
   if ((long long)b->max_len > (long long)MK_KV4_PAGE * b->max_pages) return MK_ERR_INVALID_ARG;
   if (dtype < 0 || dtype > 2) return MK_ERR_INVALID_ARG;
-  if (b->n_seqs > 65535) return MK_ERR_UNSUPPORTED;
+  if (b->n_seqs > 65535 || b->max_new > (1 << 27)) return MK_ERR_UNSUPPORTED;  // (row indexes times 8 query heads)
   return MK_OK;
 }
 

@@ -88,9 +88,10 @@ __device__ __forceinline__ uint8_t* kv4_tile(const mk_kv4_cache& c, const int32_
 
 // Waits for a phase of an mbarrier, a bounded number of tries; on expiry the cache's
 // status word says so.  A look first (27 cycles where the phase is over, the suspending
-// try takes 100), then tries that may suspend the thread for 10 us (spinning instead takes
+// try takes 100), then tries that suspend the thread for a while, 4 us measured, so about a second
+// in all (spinning instead takes
 // issue slots from the other warps: a 2048-token prompt 79 -> 82 us).
-constexpr int kKv4Tries = 1 << 20;
+constexpr int kKv4Tries = 1 << 18;
 __device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
   uint32_t over;
   asm volatile(
@@ -245,13 +246,15 @@ static __device__ __noinline__ uint32_t kv4_codes_exact(float x0, float x1, floa
 __device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], uint32_t params, float inv) {
   const float z = h_hi(params), zi = -z * inv;
   if (inv == 0.f) return 0u;  // all equal, or NaN
-  uint32_t codes = 0;
+  // (the shifted bits of kRound are taken off together: one instruction per code)
+  constexpr uint32_t kBias = 0x4B400000u * 0x11111111u;
+  uint32_t codes = 0u - kBias;
   float off = 0.f;  // largest distance from an integer
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = fmaf(x[i], inv, zi), n = t + kRound;
     off = fmaxf(off, fabsf(t - (n - kRound)));
-    codes += (__float_as_uint(n) - __float_as_uint(kRound)) << (4 * i);
+    codes += __float_as_uint(n) << (4 * i);
   }
   // t is off by 2^-24 of z / s (rounded once) and, t being below 16, by 16 (2^-23 + 2^-24)
   if (off > 0.5f - fmaf(fabsf(zi), 1.2e-7f, 3.9e-6f))  // some value is next to a border
