@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libmk.so")
 OBJ = os.path.join(ROOT, "_build", "obj")
 # (object name, source, extra flags)
 UNITS = [
-    ("mk_api", "mk_api.cu", []),
+    ("mk_kv4_slot", "mk_kv4_slot.cu", []),  # includes mk_api.cu
     ("mk_sched", "mk_sched.cpp", []),
     ("mk_noalloc", "mk_noalloc.cu", []),
     ("mk_engines", "mk_engines.cu", []),
@@ -32,7 +32,7 @@ UNITS = [
     ("mk_kv4_prompt", "mk_kv4_prompt.cu", []),
 ] + [(f"mk_inst_s{s}_n{n}", "mk_inst.cu", [f"-DMK_SPEC={s}", f"-DMK_NBT={n}"])
      for s in (0, 1, 2) for n in (8, 4, 2, 1)]
-DEPS = ["mk_kernel.cuh", "mk_device.cuh", "mk_matvec.cuh", "mk_plan.h", "mk_tc.cuh", "mk_kv4.cuh", "mk_kv4.h"]
+DEPS = ["mk_kernel.cuh", "mk_device.cuh", "mk_matvec.cuh", "mk_plan.h", "mk_tc.cuh", "mk_kv4.cuh", "mk_kv4.h", "mk_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC"]
 
