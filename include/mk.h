@@ -396,8 +396,8 @@ int64_t mk_kv4_page_bytes(int32_t head_dim);
 mk_status mk_kv4_append(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
                         const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream);
 
-/* Read the same rows back: the values the cache stands for, rounded to dtype.
- * Asynchronous. */
+/* Read the same rows back: the values the cache stands for, rounded to dtype.  The
+ * two outputs must not share memory.  Asynchronous. */
 mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
                       const mk_kv4_rows* k, const mk_kv4_rows* v, int32_t dtype, void* stream);
 
@@ -409,8 +409,8 @@ mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_bat
  * One new token per sequence or a few, whole prompts, and any mix run here; work is
  * split along the positions when there are few rows, which takes `workspace` (device,
  * 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when that is 0): concurrent
- * calls need one each, and nothing is kept in it.  q and out have type dtype.
- * Asynchronous. */
+ * calls need one each, and nothing is kept in it.  q and out have type dtype; out may be
+ * q itself.  Asynchronous. */
 mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
                            const mk_kv4_rows* q, const mk_kv4_rows* out, int32_t n_heads, int32_t dtype,
                            float scale, void* workspace, int64_t workspace_bytes, void* stream);

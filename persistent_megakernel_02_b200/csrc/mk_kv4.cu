@@ -278,6 +278,7 @@ mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, 
   st = kv4_check_rows(k, dtype, b->n_rows, c->n_kv_heads, c->head_dim, !WRITE);
   if (st == MK_OK) st = kv4_check_rows(v, dtype, b->n_rows, c->n_kv_heads, c->head_dim, !WRITE);
   if (st != MK_OK) return st;
+  if (!WRITE && k->p == v->p) return MK_ERR_INVALID_ARG;  // one output for both
   const int size = dtype == 2 ? 4 : 2;
   BatchRows rows;
   const mk_kv4_rows* kv[2] = {k, v};

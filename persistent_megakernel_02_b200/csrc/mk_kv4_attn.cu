@@ -935,7 +935,7 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
                                       float scale, void* workspace, int64_t workspace_bytes, void* stream) {
   mk_status st = check_attention(cache, layer, batch, n_heads, dtype);
   if (st != MK_OK) return st;
-  if (!std::isfinite(scale)) return MK_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * 1.44269504088896341f)) return MK_ERR_INVALID_ARG;
   if (batch->n_rows == 0) return MK_OK;
   st = kv4_check_rows(q, dtype, batch->n_rows, n_heads, cache->head_dim, false);
   if (st == MK_OK) st = kv4_check_rows(out, dtype, batch->n_rows, n_heads, cache->head_dim, true);

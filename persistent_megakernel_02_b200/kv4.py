@@ -141,12 +141,13 @@ class Kv4Cache:
         self._kv(self._append, "mk_kv4_append", layer, k, v, batch, stream)
 
     def read(self, layer, k, v, batch, stream=None):
-        """Write the values the cache holds for the batch's rows into ``k`` and ``v``."""
+        """Write the values the cache holds for the batch's rows into ``k`` and ``v``, which
+        must not share memory."""
         self._kv(self._read, "mk_kv4_read", layer, k, v, batch, stream)
 
     def attend(self, layer, q, out, batch, scale=None, workspace=None, stream=None):
         """Causal attention of query rows ``q`` [n_rows, n_heads, head_dim] over the cache,
-        each row seeing the positions up to its own; ``out`` like ``q``.  ``scale`` defaults to
+        each row seeing the positions up to its own; ``out`` like ``q``, or ``q`` itself.  ``scale`` defaults to
         1 / sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of ``workspace_bytes`` for calls
         that must not allocate; otherwise one is allocated on the launch stream."""
         what = "mk_kv4_attention"

@@ -468,6 +468,61 @@ def test_a_captured_step_replays_as_the_sequence_grows(new):
     cache.check()
 
 
+@pytest.mark.parametrize("n_len,new,kv_heads", [(9000, 1, 2), (1500, 1, 16), (6000, 200, 2), (700, 300, 16)])
+def test_a_captured_call_of_every_form_replays(n_len, new, kv_heads):
+    """Splits joined by a second launch, by a cluster, a prompt split along the cache, a prompt not split: captured
+    without a call before, replayed with other queries."""
+    s = Setup(64, kv_heads, [n_len], [new])
+    kv = s.fill()
+    q = s.rand(s.rows, 4 * kv_heads, "bf16")
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.cache.attend(0, q, out, s.batch)
+    for _ in range(2):
+        q.copy_(s.rand(s.rows, 4 * kv_heads, "bf16"))
+        out.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(s, kv, q, out, "bf16")
+    s.cache.check()
+
+
+@pytest.mark.parametrize("lens,new,kv_heads", [([9000, 70], [1, 1], 2), ([1500], [1], 16), ([6000], [200], 2), ([700, 300], [300, 5], 16)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_output_may_be_the_queries(lens, new, kv_heads, dtype):
+    s = Setup(64, kv_heads, lens, new)
+    kv = s.fill()
+    q = s.rand(s.rows, 4 * kv_heads, dtype)
+    same = q.clone()
+    s.cache.attend(0, same, same, s.batch)
+    check_attention(s, kv, q, same, dtype)
+
+
+@pytest.mark.parametrize("new", [[2, 1], [300, 200]])
+def test_rows_before_the_first_sequence_are_left_alone(new):
+    """cu may start behind row 0: rows no sequence owns are neither read nor written."""
+    s = Setup(64, 8, [400, 350], new)
+    kv = s.fill()
+    cu = s.cu + 3
+    batch = s.cache.batch(cu, s.kv_lens, s.rows + 3, max(new), s.max_len)
+    q = torch.cat([torch.full((3, 32, 64), float("nan"), dtype=torch.bfloat16, device="cuda"), s.rand(s.rows, 32, "bf16")])
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, out, batch)
+    assert (out[:3] == -7.0).all()
+    check_attention(s, kv, q[3:], out[3:], "bf16")
+    k, v = (torch.full((s.rows + 3, 8, 64), -7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    s.cache.read(0, k, v, batch)
+    s.cache.check()
+    assert (k[:3] == -7.0).all() and (v[:3] == -7.0).all()
+    at = 3
+    for (kk, vv), n in zip(kv, new):
+        for t, x in ((k, kk), (v, vv)):
+            assert torch.equal(t[at:at + n].cpu(), torch.from_numpy(x[len(x) - n:]).float().bfloat16())
+        at += n
+
+
 # ---- what the device finds wrong ---------------------------------------------------------
 
 
@@ -535,10 +590,12 @@ def test_refusals():
     flat = torch.zeros(40 * 2 * 64 + 1, dtype=torch.bfloat16, device="cuda")
     refused(s.cache.append, 0, flat[1:].view(40, 2, 64), k, s.batch)  # not 16-byte aligned
     refused(s.cache.read, 0, k[:1].expand(40, 2, 64), k, s.batch)     # an output that overlaps itself
+    refused(s.cache.read, 0, k, k, s.batch)                           # one output for both
     refused(s.cache.attend, 0, q, torch.empty_like(q).float(), s.batch)
     refused(s.cache.attend, 0, s.rand(40, 3, "bf16"), s.rand(40, 3, "bf16"), s.batch)
     refused(s.cache.attend, 0, s.rand(40, 32, "bf16"), s.rand(40, 32, "bf16"), s.batch)  # 16 per kv head
     refused(s.cache.attend, 0, q, torch.empty_like(q), s.batch, scale=float("nan"))
+    refused(s.cache.attend, 0, q, torch.empty_like(q), s.batch, scale=3e38)
     refused(s.cache.attend, 0, q[:, :, ::2], torch.empty_like(q), s.batch)
     refused(Kv4Cache, s.cache.pool, s.table, 128)
     refused(Kv4Cache, s.cache.pool.cpu(), s.table, 64)

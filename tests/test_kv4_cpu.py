@@ -81,6 +81,7 @@ def test_calls_refuse_bad_numbers():
     c, b, r = _args()
     lib = mk.lib()
     n = ctypes.c_int64()
+    assert lib.mk_kv4_read(c, 0, b, r, r, 0, None) == 1  # one output for both
     for layer in (-1, 2):
         assert lib.mk_kv4_append(c, layer, b, r, r, 0, None) == 1
         assert lib.mk_kv4_attention(c, layer, b, r, r, 2, 0, 0.1, None, 0, None) == 1
@@ -89,7 +90,7 @@ def test_calls_refuse_bad_numbers():
         assert lib.mk_kv4_attention_workspace(c, b, 2, dtype, ctypes.byref(n)) == 1
     for heads, want in ((0, 1), (3, 1), (6, 2), (32, 2)):
         assert lib.mk_kv4_attention(c, 0, b, r, r, heads, 0, 0.1, None, 0, None) == want
-    for scale in (float("nan"), float("inf")):
+    for scale in (float("nan"), float("inf"), 3e38):
         assert lib.mk_kv4_attention(c, 0, b, r, r, 2, 0, scale, None, 0, None) == 1
     overlap = _args(rows=dict(row_stride=64))[2]  # rows of two heads overlap
     assert lib.mk_kv4_read(c, 0, b, overlap, r, 0, None) == 1
