@@ -355,8 +355,8 @@ mk_status mk_matvec_engine_status(void* stream);
  * Memory is the caller's, as with the weights: a pool of pages of MK_KV4_PAGE
  * positions, and per batch a table of each sequence's pages.  Sequence lengths live
  * on the device, so a captured graph can be replayed while they grow; the host gives
- * their bounds.  A batch with numbers outside these bounds (cu not ascending from 0 to
- * at most n_rows, a span above max_new, a length below 0 or above max_len) or a page
+ * their bounds.  A batch with numbers outside these bounds (cu not ascending
+ * within 0 .. n_rows, a span above max_new, a length below 0 or above max_len) or a page
  * id outside the pool is recorded in the cache's status word; the sequence or page it
  * concerns is neither written nor read.  Sequences may share pages that are only
  * read; calls that overlap on the GPU, and the sequences of one call, must not write
@@ -376,7 +376,7 @@ typedef struct {
   const int32_t* cu;           /* device [n_seqs + 1]: rows cu[i] .. cu[i + 1] - 1 belong to sequence i */
   const int32_t* kv_lens;      /* device [n_seqs]: length in the cache, these rows included */
   int32_t n_seqs, max_pages;
-  int32_t n_rows;              /* rows of the tensors; those from cu[n_seqs] on are left alone */
+  int32_t n_rows;              /* rows of the tensors; those before cu[0] and from cu[n_seqs] on are left alone */
   int32_t max_new;             /* bound of cu[i + 1] - cu[i] */
   int32_t max_len;             /* bound of kv_lens, at most 64 * max_pages */
 } mk_kv4_batch;

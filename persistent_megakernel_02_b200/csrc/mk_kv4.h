@@ -1,5 +1,6 @@
 // mk_kv4.h -- host-side pieces of the 4-bit KV cache shared by its translation units
-// and by the handle (mk_api.cu).
+// and by the handle's park and resume
+// (mk_kv4_slot.cu).
 #pragma once
 
 #include <cuda_runtime.h>

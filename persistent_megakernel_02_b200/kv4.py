@@ -60,9 +60,9 @@ class Kv4Batch:
         max_pages = int(block_table.shape[1])
         if n_rows < 0 or max_new < 0 or not 0 <= max_len <= PAGE * max_pages or max(n_rows, max_len) >= 2**31:
             _bad("Kv4Batch", f"bounds: 0 <= n_rows, 0 <= max_new, 0 <= max_len <= {PAGE} * {max_pages}")
-        self.n_rows = int(n_rows)
+        self.n_rows, self.device = int(n_rows), cache.device
         self._keep = (block_table, cu, kv_lens)
-        self._workspace_bytes = {}
+        self._workspace_bytes = {}  # by cache shape, heads and type: caches of other shapes may share a batch
         self._struct = MkKv4Batch(block_table.data_ptr(), cu.data_ptr(), kv_lens.data_ptr(), n, max_pages,
                                   int(n_rows), min(int(max_new), int(n_rows)), int(max_len))
 
@@ -88,6 +88,7 @@ class Kv4Cache:
         self._struct = MkKv4CacheStruct(pool.data_ptr(), self._status.data_ptr(), self.n_layers, self.n_pages,
                                         self.n_kv_heads, self.head_dim)
         self._index = pool.device.index
+        self._shape = (self.n_kv_heads, self.head_dim)
         self._scale = 1.0 / math.sqrt(head_dim)
         so = lib()
         self._append, self._read, self._attention = so.mk_kv4_append, so.mk_kv4_read, so.mk_kv4_attention
@@ -106,9 +107,11 @@ class Kv4Cache:
         return Kv4Batch(self, self.block_table if block_table is None else block_table, cu, kv_lens, n_rows,
                         max_new, max_len)
 
-    def _launch(self, what, stream):
+    def _launch(self, what, stream, batch=None):
         if _current_device() != self._index:
             _bad(what, f"the cache is not on the current CUDA device ({torch.cuda.current_device()})")
+        if batch is not None and batch.device != self.device:
+            _bad(what, f"the batch must be on {self.device}")
         if stream is None:
             return _current_stream(self._index)
         return getattr(stream, "cuda_stream", stream)
@@ -131,7 +134,7 @@ class Kv4Cache:
         dtype = k.dtype
         kr = self._rows(what, "k", k, self.n_kv_heads, batch, dtype)
         vr = self._rows(what, "v", v, self.n_kv_heads, batch, dtype)
-        st = fn(self._struct, layer, batch._struct, kr, vr, _DTYPES[dtype], self._launch(what, stream))
+        st = fn(self._struct, layer, batch._struct, kr, vr, _DTYPES[dtype], self._launch(what, stream, batch))
         if st:
             raise MkError(st, what)
 
@@ -155,8 +158,8 @@ class Kv4Cache:
         heads = q.shape[1] if q.dim() == 3 else 0
         qr = self._rows(what, "q", q, heads, batch, dtype)
         orow = self._rows(what, "out", out, heads, batch, dtype)
-        raw = self._launch(what, stream)
-        need = batch._workspace_bytes.get((heads, dtype))
+        raw = self._launch(what, stream, batch)
+        need = batch._workspace_bytes.get((self._shape, heads, dtype))
         if need is None:
             need = self.workspace_bytes(batch, heads, dtype)
         ptr = None
@@ -178,12 +181,12 @@ class Kv4Cache:
 
     def workspace_bytes(self, batch, n_heads, dtype) -> int:
         """Workspace of :meth:`attend` for this batch (0 where it needs none)."""
-        got = batch._workspace_bytes.get((n_heads, dtype))
+        got = batch._workspace_bytes.get((self._shape, n_heads, dtype))
         if got is None:
             n = ctypes.c_int64()
             _check(lib().mk_kv4_attention_workspace(self._struct, batch._struct, n_heads, _DTYPES.get(dtype, -1),
                                                     ctypes.byref(n)), "mk_kv4_attention_workspace")
-            got = batch._workspace_bytes[(n_heads, dtype)] = n.value
+            got = batch._workspace_bytes[(self._shape, n_heads, dtype)] = n.value
         return got
 
     def check(self, stream=None):

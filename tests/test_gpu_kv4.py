@@ -500,6 +500,24 @@ def test_the_output_may_be_the_queries(lens, new, kv_heads, dtype):
     check_attention(s, kv, q, same, dtype)
 
 
+def test_caches_of_other_shapes_share_a_batch():
+    """Two models over the same sequences: the workspace is the called cache's."""
+    from persistent_megakernel_02_b200 import Kv4Cache
+
+    sets = [Setup(d, kvh, [9000], [1], seed=3) for d, kvh in ((64, 32), (64, 4), (128, 4))]
+    shared = sets[0].batch
+    needs = set()
+    for s in sets + sets[::-1]:
+        kv = s.fill()
+        s.cache = Kv4Cache(s.cache.pool, s.table, s.d)
+        q = s.rand(1, 32, "bf16")
+        out = torch.empty_like(q)
+        needs.add(s.cache.workspace_bytes(s.batch, 32, torch.bfloat16))
+        s.cache.attend(0, q, out, shared)
+        check_attention(s, kv, q, out, "bf16")
+    assert len(needs) > 1
+
+
 @pytest.mark.parametrize("new", [[2, 1], [300, 200]])
 def test_rows_before_the_first_sequence_are_left_alone(new):
     """cu may start behind row 0: rows no sequence owns are neither read nor written."""
