@@ -52,7 +52,10 @@ struct PSmem {
 struct PShared {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], w_full[2][2], wv_done[2], o_full[2], drained[2];
   uint32_t tmem;
-  uint32_t bad[2][4];  // blocks of 32 positions whose page id is out of range
+  // Blocks of 32 positions whose page id is out of range.  By tile modulo 4: K's buffer is free
+  // once the scores are computed, which is before they are masked, so that a tile's flags have
+  // to outlive the next tile's but one (the one behind that starts after they have been read).
+  uint32_t bad[4][4];
   // first position whose V is NaN, by group: it is zero in the product (0 x NaN would reach
   // rows that do not see it) and put into the rows that see it at the end
   int nan_first[4];
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       uint32_t s[64];
       tmem_get64(ts + 64 * h, s);
       const int base = p0 + i * 64, left = lim - base;  // columns with position < left are seen
-      const uint32_t bad0 = sh.bad[buf][2 * h], bad1 = sh.bad[buf][2 * h + 1];
+      const uint32_t bad0 = sh.bad[(i >> 1) & 3][2 * h], bad1 = sh.bad[(i >> 1) & 3][2 * h + 1];
       float mx;
       if (whole && base + 64 <= lim_warp && (bad0 | bad1) == 0) {
         float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       uint8_t* sk = skv + buf * 2 * PSmem<D>::kKV;
       if (lane == 0) {
         const bool bad = page != -2 && (unsigned)page >= (unsigned)a.c.n_pages;
-        sh.bad[buf][w] = bad;
+        sh.bad[j & 3][w] = bad;
         if (bad) atomicOr(a.c.status, KV4_BAD_PAGE);
       }
 #pragma unroll

@@ -385,6 +385,28 @@ def test_missing_pages_of_a_prompt_are_reported_and_masked():
     assert (err <= R.tolerance(want, reach, np.abs(v).max(), "bf16")).all()
 
 
+@pytest.mark.parametrize("d,kv_heads,new", [(64, 16, 400), (128, 16, 300), (64, 2, 400), (64, 8, 1), (64, 8, 40)])
+def test_missing_pages_of_a_long_cache_are_left_out(d, kv_heads, new):
+    """Pages missing here and there: each block is masked by its own page's flag."""
+    from persistent_megakernel_02_b200 import MkError
+
+    n_len, gone = 2500, (3, 10, 11, 18, 24, 31)  # all before the first query
+    s = Setup(d, kv_heads, [n_len], [new])
+    kv = s.fill()
+    q = s.rand(s.rows, 2 * kv_heads, "bf16")
+    out = torch.empty_like(q)
+    for i, page in enumerate(gone):
+        s.table[0, page] = s.cache.n_pages + i if i % 2 else -1 - i
+    rest = np.concatenate([np.arange(64 * p, 64 * p + 64) for p in gone])
+    kv = [tuple(np.delete(x, rest, 0) for x in kv[0])]
+    t = Setup(d, kv_heads, [n_len - len(rest)], [new])  # the same as without them
+    for _ in range(3):
+        s.cache.attend(0, q, out, s.batch)
+        with pytest.raises(MkError, match="DEVICE_FAULT"):
+            s.cache.check()
+        check_attention(t, kv, q, out, "bf16")
+
+
 @pytest.mark.parametrize("kv_heads,lens,new", [(2, [90, 300], [40, 1]), (8, [500] * 4, [300] * 4)])
 def test_attention_with_other_strides(kv_heads, lens, new):
     s = Setup(128, kv_heads, lens, new, layers=2)
