@@ -776,7 +776,7 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   const long long rows = std::max<long long>(b->max_new, 1) * rep;  // 0: still looks at the spans
   // Many rows of 16-bit types: 256-row tiles on tcgen05, where that is expected to be
   // faster.  Measured (one B200, us, 64- / 128-value heads): there a tile of 128 positions takes
-  // 1.85 / 2.2 and a CTA 6 more, one CTA on an SM, and a join 5 and 0.35 per split; here
+  // 1.85 / 2.2 (fp16 2.15 / 2.75) and a CTA 6 more, one CTA on an SM, and a join 5 and 0.35 per split; here
   // 16 rows x 16 positions take 0.00033 / 0.00062 of the whole GPU, and a call 10 more.  E.g.
   // 8 kv heads x 4 query heads over 16384 positions, 64 values: 16 new tokens 24 here, 27
   // there; 128 tokens 106 here, 243 there unsplit, 45 split; 512 tokens 334, 248, 134.
@@ -790,7 +790,8 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
     const long long n_split = std::max(1ll, std::min(sms / std::max(base, 1ll), tiles / 4));
     const long long per = std::max(1ll, (tiles + n_split - 1) / n_split);
     const double here = 10 + (double)seq_heads * ((rows + 15) / 16) * ((b->max_len + 15) / 16) * (wide ? 0.00062 : 0.00033);
-    const double there = (double)((base * n_split + sms - 1) / sms) * (6 + per * (wide ? 2.2 : 1.85)) + (n_split > 1 ? 5 + 0.35 * n_split : 0);
+    const double tile = dtype == 0 ? (wide ? 2.2 : 1.85) : wide ? 2.75 : 2.15;
+    const double there = (double)((base * n_split + sms - 1) / sms) * (6 + per * tile) + (n_split > 1 ? 5 + 0.35 * n_split : 0);
     if (there < here) {
       p->prompt = true;
       p->cluster = false;

@@ -12,16 +12,20 @@
 // half's scores are under way meanwhile, K's buffers are freed apart from V's, and each
 // query tile has an issuing warp of its own, so that neither waits for the other.
 //
-// K and V are z + s c rounded once to fp16 (2^-12: 16-bit types only), queries are scaled
-// by a power of two per row, which is exact in fp16 but for values 2^-24 below the row's
-// largest, weights are rounded to fp16.  The order of values inside 8 and of positions
-// inside 32 is the one the codes come in: queries are permuted alike, and S, W and V
-// share the order of positions.  O is rescaled only when a score passes the row's
-// reference by more than 16x.
+// For bf16 calls K and V are z + s c rounded once to fp16 (2^-11, an eighth of the output's
+// own rounding).  For fp16 calls that would show, K's most of all, as it grows with the scores:
+// there K, and V of 64-value heads, are two fp16 parts, good to 2^-17 together, and take two
+// products.  Errors in the 2-norm, 2048 tokens over 8192 positions: 7.2e-4 rounded, 2.9e-4 so,
+// the output's own rounding 2.1e-4; 217 us became 254, with 128-value heads 292 became 366
+// (V in two parts too: 572).  Queries are scaled by a power of two per row, which is exact in
+// fp16 but for values 2^-24 below the row's largest, weights are rounded to fp16.  The order
+// of values inside 8 and of positions inside 32 is the one the codes come in: queries are
+// permuted alike, and S, W and V share the order of positions.  O is rescaled only when a
+// score passes the row's reference by more than 16x.
 //
 // Bound: with 64-value heads the exponentials, 16 per SM and cycle: 2048 cycles for the
 // 256 x 128 scores of a tile, 1024 for its products.  A tile takes about 3500 (1.85 us), the
-// warps' instructions in between: 2048 tokens x 32 heads over 8192 positions 217 us, 550
+// warps' instructions in between: 2048 bf16 tokens x 32 heads over 8192 positions 216 us, 550
 // TFLOP/s; 2048 tokens of 128-value heads, causal, 55 us, 620 TFLOP/s.  (Three or four
 // query tiles, which would fill the exponential unit, do not fit tensor memory; sixteen
 // softmax warps for the two, 32 columns each, measured 267 us for the former.)
@@ -42,15 +46,20 @@ constexpr int kPTile = 128;  // positions per tile, and rows per query tile
 constexpr int kPHead = 4;    // log2 of what a weight may pass the reference by
 constexpr int kPLift = 10;   // weights are 2^(score - m + kPLift), at most 2^14
 
-template <int D>
+// K and V buffers: two of a tile; where K's or V's values have two parts they are of a half
+// tile, and four of them with 64-value heads.  (With 128-value heads there is room for two
+// halves of K and no more: with V in two parts as well the buffers wait for one another.)
+template <int D, class T>
 struct PSmem {
-  static constexpr int kQ = 2 * kPTile * D * 2;   // both query tiles
-  static constexpr int kKV = kPTile * D * 2;      // one K or V tile
-  static constexpr int kBytes = 1024 + kQ + 4 * kKV;
+  static constexpr bool kK2 = std::is_same<T, __half>::value, kV2 = kK2 && D == 64;
+  static constexpr int kQ = D == 64 ? 0 : 2 * kPTile * D * 2;  // both query tiles, if not in tensor memory
+  static constexpr int kKV = kPTile * D * 2;      // one K or V buffer
+  static constexpr int kBufs = kV2 ? 4 : 2;
+  static constexpr int kBytes = 1024 + kQ + 2 * kBufs * kKV;
 };
 
 struct PShared {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], w_full[2][2], wv_done[2], o_full[2], drained[2];
+  uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2][2], w_full[2][2], wv_done[2], o_full[2], drained[2];
   uint32_t tmem;
   // Blocks of 32 positions whose page id is out of range.  By tile modulo 4: K's buffer is free
   // once the scores are computed, which is before they are masked, so that a tile's flags have
@@ -164,6 +173,40 @@ __device__ __forceinline__ void dequant8(uint32_t x, uint32_t s2, uint32_t z2, u
   v[2] = hfma2(hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE400E400u), s2, z2);
   v[3] = hfma2(hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u), s2, z2);
 }
+// The same as two fp16 values: hi = z_a + s_hi c, exact, and lo = z_b + s_lo c, with s_hi and z_a
+// the multiples of a grid nearest to s and z, and s_lo, z_b what is left.  With 2^e the leading
+// bit of the group's largest value the grid is 2^(e - 8): hi is at most 2^9 + 8 of its steps,
+// lo at most 8, where rounding it to fp16 is 2^-17 of the largest.  Rounding to the grid:
+// adding 1.5 x 2^10 of its steps and taking them off again.
+struct Params {
+  uint32_t sh, za, sl, zb;
+};
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) { return hadd2(a, b ^ 0x80008000u); }
+__device__ __forceinline__ Params split_params(uint32_t s2, uint32_t z2) {
+  const uint32_t end = hfma2(s2, 0x4B804B80u, z2) & 0x7FFF7FFFu, low = z2 & 0x7FFF7FFFu;  // |z + 15 s|, |z|
+  const uint32_t top = __vmaxu2(end, low);  // (as integers: their order is that of the values)
+  uint32_t big = (top & 0x7C007C00u) + 0x0A000A00u;
+  big &= __vcmpleu2(big, 0x7A007A00u);  // (from 2^14 on, where the sum could overflow, hi is rounded once)
+  const uint32_t bz = big | (~z2 & 0x80008000u);  // of the other sign than z: no overflow either
+  Params p;
+  p.sh = hsub2(hadd2(s2, big), big);
+  p.sl = hsub2(s2, p.sh);
+  p.za = hsub2(hadd2(z2, bz), bz);
+  p.zb = hsub2(z2, p.za);
+  return p;
+}
+__device__ __forceinline__ void dequant8(uint32_t x, const Params& p, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  const uint32_t y = x >> 8;
+  const uint32_t c[4] = {hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE400E400u),
+                         hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u),
+                         hadd2((y & 0x000F000Fu) | 0x64006400u, 0xE400E400u),
+                         hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = hfma2(c[i], p.sh, p.za);
+    lo[i] = hfma2(c[i], p.sl, p.zb);
+  }
+}
 __device__ __forceinline__ uint32_t both(uint32_t pair, int which) {  // one half of a pair, twice
   return __byte_perm(pair, 0u, which ? 0x3232 : 0x1010);
 }
@@ -182,12 +225,19 @@ template <int D, class T>
 __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a) {
   using L = Kv4<D>;
   constexpr int G = L::G;
+  constexpr uint32_t kPart = D * 128;  // bytes of a half, or of a part of one
+  using M = PSmem<D, T>;
+  constexpr bool kK2 = M::kK2, kV2 = M::kV2;  // values in two parts
+  constexpr int kBufs = M::kBufs;
   constexpr uint32_t kIdQK = idesc_f16(128, 64), kIdWV = idesc_f16(128, D);
   extern __shared__ uint8_t smem_raw[];
   __shared__ PShared sh;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sq = smem;                    // [2][D / 64][128 rows][128 bytes]
-  uint8_t* skv = smem + PSmem<D>::kQ;    // [2 buffers][K, V]
+  // [buffers][K, V]: a tile each (K [D / 64][128 rows][128 bytes], V [2 halves][D rows][128
+  // bytes]), or where there are two parts a half of 64 positions each (K [hi, lo][D / 64][64
+  // rows][128 bytes], V [hi, lo][D rows][128 bytes])
+  uint8_t* skv = smem + M::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   int idx = blockIdx.x;
@@ -217,11 +267,13 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
   if (tid < 4) sh.nan_first[tid] = 0x7FFFFFFF;
   if (tid == 0) {
     mbar_init(&sh.q_full, 2 * kPTile);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], kPTile);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(&sh.k_full[i], kK2 ? kPTile / 2 : kPTile);
       mbar_init(&sh.k_empty[i], 2);
-      mbar_init(&sh.v_full[i], kPTile);
+      mbar_init(&sh.v_full[i], kV2 ? kPTile / 2 : kPTile);
       mbar_init(&sh.v_empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
       for (int h = 0; h < 2; ++h) {
         mbar_init(&sh.s_full[i][h], 1);
         mbar_init(&sh.w_full[i][h], 4);
@@ -239,7 +291,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
   // Columns: S0, S1 128 each (two halves of 64 positions), O0, O1 D each.  The weights of a
   // half, 32 columns, lie over the scores of that half.
   const uint32_t tmem = sh.tmem;
-  constexpr uint32_t kO = 256;
+  // 64-value queries, 32 columns a tile, are behind them (from shared memory their reads hold
+  // up the products: fp16 275 us there for 2048 tokens over 8192 positions, 258 here).
+  constexpr uint32_t kO = 256, kQ = 384;
+  constexpr bool kQT = D == 64;
 
   if (warp < 8) {
     // ---------------- softmax: one thread per row ----------------
@@ -268,6 +323,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       // the maximum of the accumulated scores is the maximum of the scores
       const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23), sup = a.scale_log2 < 0.f ? -up : up;
+      [[maybe_unused]] uint32_t qt[16];
       kscale = fmaxf(fabsf(a.scale_log2) / up, 1e-37f);  // (never zero: it multiplies the -inf of masked positions)
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
@@ -275,11 +331,22 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
         unpack8(raw[c], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= sup;
-        *reinterpret_cast<uint4*>(sq + (t * (D / 64) + c / 8) * 16384 + chunk_at(r_in, c % 8)) =
-            make_uint4(pack_h(x[0], x[4]), pack_h(x[1], x[5]), pack_h(x[2], x[6]), pack_h(x[3], x[7]));
+        if constexpr (kQT) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qt[4 * (c & 3) + i] = pack_h(x[i], x[i + 4]);
+          if ((c & 3) == 3) tmem_st16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kQ + t * 32 + 4 * (c - 3), qt);
+        } else {
+          *reinterpret_cast<uint4*>(sq + (t * (D / 64) + c / 8) * 16384 + chunk_at(r_in, c % 8)) =
+              make_uint4(pack_h(x[0], x[4]), pack_h(x[1], x[5]), pack_h(x[2], x[6]), pack_h(x[3], x[7]));
+        }
       }
     }
-    fence_proxy_async_smem();
+    if constexpr (kQT) {
+      tmem_st_wait();
+      tc_fence_before();
+    } else {
+      fence_proxy_async_smem();
+    }
     mbar_arrive(&sh.q_full);
 
     const int lim = live ? start + row / a.rep + 1 : 0;               // positions this row sees
@@ -446,10 +513,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
     bool ok = true;
     // K of tile j: row of position 16 u + 8 n + gid of the block (column order), 16 bytes per word
     auto put_k = [&](int j, int page) {
-      const int buf = j & 1;
-      if (j >= 2) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.k_empty[buf], ((j >> 1) - 1) & 1, a.c.status));
+      const int b = kK2 ? 2 * j + (w >> 1) : j, buf = b % kBufs, before = b / kBufs - 1;  // its use before
+      if (before >= 0) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.k_empty[buf], before & 1, a.c.status));
       if (!ok) return;
-      uint8_t* sk = skv + buf * 2 * PSmem<D>::kKV;
+      uint8_t* sk = skv + buf * 2 * M::kKV;
       if (lane == 0) {
         const bool bad = page != -2 && (unsigned)page >= (unsigned)a.c.n_pages;
         sh.bad[j & 3][w] = bad;
@@ -459,16 +526,28 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const int r = 32 * w + 8 * (gid >> 1) + 4 * u + 2 * n + (gid & 1);
+          const int r = 32 * (kK2 ? w & 1 : w) + 8 * (gid >> 1) + 4 * u + 2 * n + (gid & 1);
           const uint32_t* c = reinterpret_cast<const uint32_t*>(kc[u]);
           const uint32_t* s = reinterpret_cast<const uint32_t*>(&ks[u][n]);
           const uint32_t* z = reinterpret_cast<const uint32_t*>(&kz[u][n]);
+          [[maybe_unused]] Params pp;  // of groups g, g + 1
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             uint32_t v[4];
-            dequant8(c[n * G + g], both(s[g], gid & 1), both(z[g / 2], g & 1), v);
             const int word = 4 * g + tig;
-            *reinterpret_cast<uint4*>(sk + (word >> 3) * 16384 + chunk_at(r, word & 7)) = make_uint4(v[0], v[1], v[2], v[3]);
+            if constexpr (kK2) {
+              if (g % 2 == 0) pp = split_params(__byte_perm(s[g], s[g + 1], gid & 1 ? 0x7632 : 0x5410), z[g / 2]);
+              const Params p{both(pp.sh, g & 1), both(pp.za, g & 1), both(pp.sl, g & 1), both(pp.zb, g & 1)};
+              uint32_t lo[4];
+              uint8_t* to = sk + (word >> 3) * 8192 + chunk_at(r, word & 7);
+              dequant8(c[n * G + g], p, v, lo);
+              *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(to + kPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+              dequant8(c[n * G + g], both(s[g], gid & 1), both(z[g / 2], g & 1), v);
+              *reinterpret_cast<uint4*>(sk + (word >> 3) * 16384 + chunk_at(r, word & 7)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
         }
       fence_proxy_async_smem();
@@ -476,7 +555,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
     };
     // V of tile j transposed: row of value 32 g + 4 gid + i, 8 positions (16 bytes) per lane
     auto put_v = [&](int j, int page) {
-      const int buf = j & 1, first = p0 + j * kPTile + 32 * w;
+      const int b = kV2 ? 2 * j + (w >> 1) : j, buf = b % kBufs, before = b / kBufs - 1;
+      const int first = p0 + j * kPTile + 32 * w;
       const int left = (unsigned)page < (unsigned)a.c.n_pages ? see - first : 0;  // positions of the block that exist
       uint32_t odd = 0;  // a NaN among the parameters
 #pragma unroll
@@ -511,38 +591,44 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
               reinterpret_cast<uint32_t*>(vs[u])[n * G + g] &= keep;
             }
       }
-      if (j >= 2) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.v_empty[buf], ((j >> 1) - 1) & 1, a.c.status));
+      if (before >= 0) ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.v_empty[buf], before & 1, a.c.status));
       if (!ok) return;
-      uint8_t* sv = skv + buf * 2 * PSmem<D>::kKV + PSmem<D>::kKV;
+      uint8_t* sv = skv + buf * 2 * M::kKV + M::kKV;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint32_t v[4][4];  // [2 u + hf][value]
+        [[maybe_unused]] uint32_t lo[4][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-            dequant8(reinterpret_cast<const uint32_t*>(vc[u])[2 * g + n],
-                     reinterpret_cast<const uint32_t*>(vs[u])[n * G + g], vz[u][g][n], v[2 * u + n]);
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t c = reinterpret_cast<const uint32_t*>(vc[u])[2 * g + n];
+            const uint32_t s = reinterpret_cast<const uint32_t*>(vs[u])[n * G + g], z = vz[u][g][n];
+            if constexpr (kV2) dequant8(c, split_params(s, z), v[2 * u + n], lo[2 * u + n]);
+            else dequant8(c, s, z, v[2 * u + n]);
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int d = 32 * g + 4 * gid + i;
-          *reinterpret_cast<uint4*>(sv + (w >> 1) * (D * 128) + chunk_at(d, 4 * (w & 1) + tig)) =
-              make_uint4(v[0][i], v[1][i], v[2][i], v[3][i]);
+          uint8_t* to = sv + (kV2 ? 0 : (w >> 1) * kPart) + chunk_at(32 * g + 4 * gid + i, 4 * (w & 1) + tig);
+          *reinterpret_cast<uint4*>(to) = make_uint4(v[0][i], v[1][i], v[2][i], v[3][i]);
+          if constexpr (kV2) *reinterpret_cast<uint4*>(to + kPart) = make_uint4(lo[0][i], lo[1][i], lo[2][i], lo[3][i]);
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.v_full[buf]);
     };
-    // K runs a tile ahead of V (its buffer is free as soon as the scores are done)
+    // K runs a tile ahead of V (its buffer is free as soon as the scores are done), but not
+    // where its buffers are two halves
+    constexpr int kAhead = kK2 && kBufs == 2 ? 0 : 1;
     int page_k = look(0), page_v = page_k, page_next = look(1);
     load_k(page_k);
     load_v(page_v);
-    for (int j = -1; j < n_max && ok; ++j) {
-      if (j + 1 < n_max) {
-        put_k(j + 1, page_k);
+    for (int j = -kAhead; j < n_max && ok; ++j) {
+      if (j + kAhead < n_max) {
+        put_k(j + kAhead, page_k);
         page_k = page_next;
         load_k(page_k);
-        page_next = look(j + 3);
+        page_next = look(j + kAhead + 2);
       }
       if (j >= 0 && ok) {
         put_v(j, page_v);
@@ -555,20 +641,44 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
     const int t = warp - 12, n = n_half[t];
     const uint32_t one = elect_one();
     const uint64_t dq = sw128_desc(smem_u32(sq) + t * (D / 64) * 16384), dk = sw128_desc(smem_u32(skv)),
-                   dv = sw128_desc(smem_u32(skv) + PSmem<D>::kKV);
-    constexpr uint32_t kBuf = 2 * PSmem<D>::kKV / 16;  // a buffer further, in the descriptor's 16-byte units
+                   dv = sw128_desc(smem_u32(skv) + M::kKV);
+    constexpr uint32_t kBuf = 2 * M::kKV / 16;  // a buffer further, in the descriptor's 16-byte units
     const uint32_t tms = tmem + t * 128, tmo = tmem + kO + t * D;
+    auto score = [&](int i, int c, uint64_t k, bool first) {  // 16 of the queries' values
+      if constexpr (kQT) mma_ts(one, tms + (i & 1) * 64, tmem + kQ + t * 32 + 8 * c, k, kIdQK, first ? 0u : 1u);
+      else mma_ss(one, tms + (i & 1) * 64, dq + (c / 4) * 1024 + (c % 4) * 2, k, kIdQK, first ? 0u : 1u);
+    };
     // scores of half i, and the product of its weights
     auto qk = [&](int i) {
+      if constexpr (kK2) {
+        const uint64_t k = dk + (uint32_t)(i % kBufs) * kBuf;
+#pragma unroll
+        for (int c = 0; c < 2 * (D / 16); ++c) {  // the parts in turn
+          const int q = c / 2;
+          score(i, q, k + (c & 1) * (kPart / 16) + (q / 4) * 512 + (q % 4) * 2, c == 0);
+        }
+        mma_commit(one, &sh.s_full[t][i & 1]);
+        mma_commit(one, &sh.k_empty[i % kBufs]);
+        return;
+      }
       const uint64_t k = dk + (uint32_t)(i >> 1 & 1) * kBuf + (uint32_t)(i & 1) * 512;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
-        mma_ss(one, tms + (i & 1) * 64, dq + (c / 4) * 1024 + (c % 4) * 2, k + (c / 4) * 1024 + (c % 4) * 2, kIdQK,
-               c ? 1u : 0u);
+        score(i, c, k + (c / 4) * 1024 + (c % 4) * 2, c == 0);
       mma_commit(one, &sh.s_full[t][i & 1]);
       if (i & 1 || i + 1 == n) mma_commit(one, &sh.k_empty[i >> 1 & 1]);  // the tile's last scores
     };
     auto wv = [&](int i) {
+      if constexpr (kV2) {
+        const uint64_t v = dv + (uint32_t)(i % kBufs) * kBuf;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          mma_ts(one, tmo, tms + (i & 1) * 64 + 8 * (c / 2), v + (c & 1) * (kPart / 16) + (c / 2) * 2, kIdWV, i || c ? 1u : 0u);
+        mma_commit(one, &sh.wv_done[t]);
+        mma_commit(one, &sh.v_empty[i % kBufs]);
+        if (i + 1 == n) mma_commit(one, &sh.o_full[t]);
+        return;
+      }
       const uint64_t v = dv + (uint32_t)(i >> 1 & 1) * kBuf + (uint32_t)(i & 1) * (D * 8);
 #pragma unroll
       for (int c = 0; c < 4; ++c) mma_ts(one, tmo, tms + (i & 1) * 64 + 8 * c, v + c * 2, kIdWV, i || c ? 1u : 0u);
@@ -576,35 +686,44 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       if (i & 1 || i + 1 == n) mma_commit(one, &sh.v_empty[i >> 1 & 1]);
       if (i + 1 == n) mma_commit(one, &sh.o_full[t]);
     };
-    auto ready = [&](uint64_t* bar, int j) {
-      const bool r = __all_sync(0xFFFFFFFFu, kv4_wait(bar + (j & 1), (j >> 1) & 1, a.c.status));
+    auto ready = [&](uint64_t* bar, int j, int bufs) {
+      const bool r = __all_sync(0xFFFFFFFFu, kv4_wait(bar + j % bufs, (j / bufs) & 1, a.c.status));
       tc_fence_after();
       return r;
     };
     bool ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.q_full, 0, a.c.status));
+    tc_fence_after();
     if (n > 0) {
-      ok = ok && ready(sh.k_full, 0);
+      ok = ok && ready(sh.k_full, 0, kBufs);
       if (ok) {
         qk(0);
-        if (n > 1) qk(1);
+        if (kK2 && n > 1) ok = ready(sh.k_full, 1, kBufs);
+        if (n > 1 && ok) qk(1);
       }
       for (int i = 0; i < n && ok; ++i) {
-        if (!(i & 1)) ok = ready(sh.v_full, i >> 1);
-        if (ok) ok = ready(sh.w_full[t], i);
+        if (kV2) ok = ready(sh.v_full, i, kBufs);
+        else if (!(i & 1)) ok = ready(sh.v_full, i >> 1, kBufs);
+        if (ok) ok = ready(sh.w_full[t], i, 2);
         if (!ok) break;
         wv(i);
         if (i + 2 < n) {
-          if (!(i & 1)) ok = ready(sh.k_full, (i + 2) >> 1);
+          if (kK2) ok = ready(sh.k_full, i + 2, kBufs);
+          else if (!(i & 1)) ok = ready(sh.k_full, (i + 2) >> 1, kBufs);
           if (ok) qk(i + 2);
         }
       }
     }
-    // tiles that only the other query tile sees: this one lets go of them as they come
-    for (int j = (n + 1) / 2; j < n_max && ok; ++j) {
-      ok = ready(sh.k_full, j);
-      if (ok && lane == 0) mbar_arrive(&sh.k_empty[j & 1]);
-      ok = ok && ready(sh.v_full, j);
-      if (ok && lane == 0) mbar_arrive(&sh.v_empty[j & 1]);
+    // tiles (or halves) that only the other query tile sees, if any: this one lets go of them as they come
+    for (int i = n; i < 2 * n_max && ok; ++i) {
+      const int k = kK2 ? i : i >> 1, v = kV2 ? i : i >> 1;
+      if (kK2 || !(i & 1)) {
+        ok = ready(sh.k_full, k, kBufs);
+        if (ok && lane == 0) mbar_arrive(&sh.k_empty[k % kBufs]);
+      }
+      if (ok && (kV2 || !(i & 1))) {
+        ok = ready(sh.v_full, v, kBufs);
+        if (ok && lane == 0) mbar_arrive(&sh.v_empty[v % kBufs]);
+      }
       __syncwarp();
     }
     if (!ok) {  // let what was issued finish before the memory goes
@@ -625,10 +744,11 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
 template <int D, class T>
 static mk_status launch(const Kv4AttnSplit& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
-  if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_prompt<D, T>), PSmem<D>::kBytes, &ready)) return MK_ERR_CUDA;
+  constexpr int kSmem = PSmem<D, T>::kBytes;
+  if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_prompt<D, T>), kSmem, &ready)) return MK_ERR_CUDA;
   const long long ctas = (long long)a.n_rt * a.c.n_kv_heads * a.b.n_seqs * a.n_split;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
-  attn_prompt<D, T><<<(unsigned)ctas, kPThreads, PSmem<D>::kBytes, s>>>(a);
+  attn_prompt<D, T><<<(unsigned)ctas, kPThreads, kSmem, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

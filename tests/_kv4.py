@@ -116,8 +116,9 @@ def tolerance(out, reach, v_max, dtype):
     32-bit tensors: queries, weights and weight * scale as two fp16 parts (2^-21 or
     better together), fp32 sums: e = 2^-20 for the scores and for the weights.
     16-bit tensors: K and V rounded to fp16 for the matrix product of prompts
-    (2^-12 each), queries exact in fp16 up to 2^-24 of the row's largest, weights fp16
-    (2^-12), weight * scale once more (2^-12): scores 2^-11, weights and V together 2^-10.
+    (2^-11 each), queries exact in fp16 up to 2^-24 of the row's largest, weights fp16
+    (2^-11), weight * scale once more (2^-11) where V is not rounded: scores 2^-11, weights
+    and V or their scales together 2^-10.
     Then the output's own rounding, half a unit in the last place (2^-24 of v_max
     stands in for its subnormals in fp16)."""
     eps = torch.finfo(DTYPES[dtype]).eps / 2
