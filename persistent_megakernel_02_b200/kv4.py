@@ -116,6 +116,10 @@ class Kv4Cache:
             return _current_stream(self._index)
         return getattr(stream, "cuda_stream", stream)
 
+    def _torch_stream(self, raw):
+        # (ExternalStream takes the default stream's 0 for none and makes a new stream)
+        return torch.cuda.ExternalStream(raw, self.device) if raw else torch.cuda.default_stream(self.device)
+
     def _rows(self, what, name, t, heads, batch, dtype):
         if (t.shape == (batch.n_rows, heads, self.head_dim) and t.dtype is dtype and dtype in _DTYPES
                 and t.get_device() == self._index):
@@ -168,8 +172,7 @@ class Kv4Cache:
                 if stream is None:
                     workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
                 else:
-                    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, self.device)
-                    with torch.cuda.stream(s):
+                    with torch.cuda.stream(self._torch_stream(raw)):
                         workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
             elif workspace.dtype != torch.uint8 or workspace.get_device() != self._index or not workspace.is_contiguous():
                 _bad(what, f"workspace must be a contiguous uint8 tensor on {self.device}")
@@ -193,7 +196,7 @@ class Kv4Cache:
         """Wait for ``stream`` and raise MkError if a call met numbers outside its batch's
         bounds or a page id outside the pool since the last check."""
         raw = self._launch("Kv4Cache.check", stream)
-        with torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device)):
+        with torch.cuda.stream(self._torch_stream(raw)):
             bits = int(self._status.item())
             self._status.zero_()
         if bits & 4:

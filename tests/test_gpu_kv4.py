@@ -563,6 +563,29 @@ def test_rows_before_the_first_sequence_are_left_alone(new):
         at += n
 
 
+@pytest.mark.parametrize("where", ["current", "default by number", "side"])
+def test_check_waits_for_its_stream(where):
+    """The status is read behind the stream's work, also where that takes a while."""
+    from persistent_megakernel_02_b200 import MkError
+
+    s = Setup(64, 2, [40], [40])
+    s.fill()
+    q = s.rand(40, 8, "bf16")
+    out = torch.empty_like(q)
+    s.table[0, 0] = s.cache.n_pages
+    work = torch.randn(8192, 8192, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    arg = {"current": None, "default by number": 0, "side": side}[where]
+    with torch.cuda.stream(side if where == "side" else torch.cuda.default_stream()):
+        for _ in range(30):  # over 20 ms
+            work @ work
+        s.cache.attend(0, q, out, s.batch, stream=arg)
+    with pytest.raises(MkError, match="DEVICE_FAULT"):
+        s.cache.check(stream=arg)
+    s.cache.check(stream=arg)
+
+
 # ---- what the device finds wrong ---------------------------------------------------------
 
 
