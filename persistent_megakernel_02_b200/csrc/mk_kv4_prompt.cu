@@ -463,10 +463,10 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
     uint4 kc[2][2 * G / 4] = {}, vc[2][2 * G / 4] = {}, vs[2][2 * G / 4] = {}, ks[2][2] = {};
     uint2 kz[2][2] = {};
     uint32_t vz[2][G][2] = {};
-    // page id of tile j, looked up a tile ahead of its loads; -2: no position there
+    // page id of tile j, looked up a tile ahead of its loads (-1 where there is no position)
     auto look = [&](int j) {
       const int p = p0 + j * kPTile + 32 * w;
-      return j < n_max && p < see ? table[p / MK_KV4_PAGE] : -2;
+      return j < n_max && p < see ? table[p / MK_KV4_PAGE] : -1;
     };
     auto tile_at = [&](int page) {
       const size_t at = (((size_t)a.layer * a.c.n_pages + page) * a.c.n_kv_heads + head) * kKv4Tiles + 2 * (w & 1);
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       if (!ok) return;
       uint8_t* sk = skv + buf * 2 * M::kKV;
       if (lane == 0) {
-        const bool bad = page != -2 && (unsigned)page >= (unsigned)a.c.n_pages;
+        const bool bad = p0 + j * kPTile + 32 * w < see && (unsigned)page >= (unsigned)a.c.n_pages;
         sh.bad[j & 3][w] = bad;
         if (bad) atomicOr(a.c.status, KV4_BAD_PAGE);
       }

@@ -407,6 +407,22 @@ def test_missing_pages_of_a_long_cache_are_left_out(d, kv_heads, new):
         check_attention(t, kv, q, out, "bf16")
 
 
+@pytest.mark.parametrize("new", [400, 1])
+@pytest.mark.parametrize("page", [-1, -2, -3, -2**31, 2**31 - 1])
+def test_every_page_id_outside_the_pool_is_reported(page, new):
+    from persistent_megakernel_02_b200 import MkError
+
+    s = Setup(64, 16, [1000], [new])
+    s.fill()
+    q = s.rand(s.rows, 32, "bf16")
+    out = torch.empty_like(q)
+    s.table[0, 3] = page
+    s.cache.attend(0, q, out, s.batch)
+    with pytest.raises(MkError, match="DEVICE_FAULT"):
+        s.cache.check()
+    assert torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("kv_heads,lens,new", [(2, [90, 300], [40, 1]), (8, [500] * 4, [300] * 4)])
 def test_attention_with_other_strides(kv_heads, lens, new):
     s = Setup(128, kv_heads, lens, new, layers=2)
