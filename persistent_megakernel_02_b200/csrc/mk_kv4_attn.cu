@@ -786,8 +786,10 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
     const bool wide = c->head_dim == 128;
     const long long n_blocks = (rows + kKv4PromptRows - 1) / kKv4PromptRows, base = n_blocks * seq_heads;
     const long long tiles = (b->max_len + 127) / 128;
-    // splits of at least four tiles, as many as keep one CTA per SM
-    const long long n_split = std::max(1ll, std::min(sms / std::max(base, 1ll), tiles / 4));
+    // splits of at least four tiles, as many as keep one CTA per SM; and of at most 256, since
+    // sums in tensor memory are cut off, not rounded: 0.7e-8 a position, measured (131072
+    // positions in one split: results 9e-4 too small)
+    const long long n_split = std::max({1ll, std::min(sms / std::max(base, 1ll), tiles / 4), (tiles + 255) / 256});
     const long long per = std::max(1ll, (tiles + n_split - 1) / n_split);
     const double here = 10 + (double)seq_heads * ((rows + 15) / 16) * ((b->max_len + 15) / 16) * (wide ? 0.00062 : 0.00033);
     const double tile = dtype == 0 ? (wide ? 2.2 : 1.85) : wide ? 2.75 : 2.15;

@@ -870,3 +870,32 @@ def test_fp16_calls_round_only_the_weights(d, kv_heads, lens, new, keys):
         a, b = s.cu_np[i], s.cu_np[i + 1]
         want, _ = reference(s, kv, q, i, scale)
         assert np.linalg.norm(got[a:b] - want) / np.linalg.norm(want) < (4.1e-4 if d == 128 else 3.3e-4)
+
+
+@pytest.mark.parametrize("d,n_len", [(64, 131072 + 77), (128, 70000)])
+def test_prompts_over_very_long_caches_keep_their_sums(d, n_len):
+    """Values with a mean of 2, so that sums grow: the mean of the relative errors.  The output's
+    rounding has no mean (16 x 8 x d of it, 2.1e-4 each: 1e-6 to 2e-6), a sum that is cut off
+    has: at most 32768 positions are added up before the parts are joined, at 2^-27 each."""
+    new, rep = 4800, 8  # enough blocks that nothing else splits the positions
+    rng = np.random.default_rng(2)
+    s = Setup(d, 1, [1], [1])
+    table = torch.from_numpy(R.tables([n_len], rng)[0]).cuda()
+    cache = type(s.cache).empty(1, int(table.shape[1]) + 2, 1, d, table)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn((n_len, 1, d), device="cuda", generator=g) + x for x in (0.0, 2.0))
+    ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n_len], [0, new], [n_len])]
+    whole = cache.batch(ints[0], ints[2], n_len, n_len, n_len)
+    cache.append(0, k, v, whole)
+    cache.read(0, k, v, whole)
+    batch = cache.batch(ints[1], ints[2], new, new, n_len)
+    q = torch.randn((new, rep, d), device="cuda", generator=g).half()
+    out = torch.empty_like(q)
+    cache.attend(0, q, out, batch)
+    cache.check()
+    at = torch.arange(n_len, device="cuda")
+    see = at[None, None, :] <= at[-16:][:, None, None]
+    sc = torch.einsum("qhd,pd->qhp", q[-16:].double(), k[:, 0].double()) * R.default_scale(d)
+    want = torch.einsum("qhp,pd->qhd", torch.softmax(sc.masked_fill(~see, -np.inf), -1), v[:, 0].double())
+    off = (out[-16:].double() - want) / want
+    assert off.mean().abs() < 32768 * 2.0**-27 + 4e-5 and off.abs().max() < 2.0**-9
