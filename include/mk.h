@@ -407,7 +407,8 @@ mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_bat
  * rep = n_heads / n_kv_heads in {1, 2, 4, 8}.  A row that sees no position (its
  * sequence is shorter than its span) is zero.  Scores, softmax and sums are fp32.
  * One new token per sequence or a few, whole prompts, and any mix run here; work is
- * split along the positions when there are few rows, which takes `workspace` (device,
+ * split along the positions when there are few rows or very many positions, which
+ * takes `workspace` (device,
  * 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when that is 0): concurrent
  * calls need one each, and nothing is kept in it.  q and out have type dtype; out may be
  * q itself.  Asynchronous. */

@@ -15,7 +15,7 @@
 // For bf16 calls K and V are z + s c rounded once to fp16 (2^-11, an eighth of the output's
 // own rounding).  For fp16 calls that would show, K's most of all, as it grows with the scores:
 // there K, and V of 64-value heads, are two fp16 parts, good to 2^-17 together, and take two
-// products.  Errors in the 2-norm, 2048 tokens over 8192 positions: 7.2e-4 rounded, 2.9e-4 so,
+// products.  Errors in the 2-norm, 2048 tokens over 8192 positions: 7.2e-4 rounded, 2.7e-4 so,
 // the output's own rounding 2.1e-4; 217 us became 254, with 128-value heads 292 became 366
 // (V in two parts too: 572).  Queries are scaled by a power of two per row, which is exact in
 // fp16 but for values 2^-24 below the row's largest, weights are rounded to fp16.  The order
