@@ -408,10 +408,9 @@ mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_bat
  * sequence is shorter than its span) is zero.  Scores, softmax and sums are fp32.
  * One new token per sequence or a few, whole prompts, and any mix run here; work is
  * split along the positions when there are few rows or very many positions, which
- * takes `workspace` (device,
- * 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when that is 0): concurrent
- * calls need one each, and nothing is kept in it.  q and out have type dtype; out may be
- * q itself.  Asynchronous. */
+ * takes `workspace` (device, 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when
+ * that is 0): concurrent calls need one each, and nothing is kept in it.  q and out have
+ * type dtype; out may be q itself.  Asynchronous. */
 mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,
                            const mk_kv4_rows* q, const mk_kv4_rows* out, int32_t n_heads, int32_t dtype,
                            float scale, void* workspace, int64_t workspace_bytes, void* stream);
