@@ -899,3 +899,28 @@ def test_prompts_over_very_long_caches_keep_their_sums(d, n_len):
     want = torch.einsum("qhp,pd->qhd", torch.softmax(sc.masked_fill(~see, -np.inf), -1), v[:, 0].double())
     off = (out[-16:].double() - want) / want
     assert off.mean().abs() < 32768 * 2.0**-27 + 4e-5 and off.abs().max() < 2.0**-9
+
+
+@pytest.mark.parametrize("new", [1, 40, 700])
+def test_pools_of_more_than_32_bits_of_bytes(new):
+    """Pages and a layer behind 2^32 bytes, and rows whose strides lead there too."""
+    from persistent_megakernel_02_b200 import Kv4Cache
+
+    d, kvh, n_len = 128, 8, 900
+    n_pages = 2**32 // (kvh * 64 * 20 * d // 16) + 50
+    table = torch.arange(n_pages - 1, n_pages - 1 - 16, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    cache = Kv4Cache.empty(2, n_pages, kvh, d, table)
+    s = Setup(d, kvh, [n_len], [new])
+    s.table, s.cache = table, cache
+    s.batch = cache.batch(s.cu, s.kv_lens, new, new, n_len)
+    kv = s.fill(layer=1)
+    far = torch.empty((2, 4 * kvh, 2**26 + d), dtype=torch.bfloat16, device="cuda")  # 128 MiB from head to head
+    q, out = (far[i].as_strided((new, 4 * kvh, d), (d, 2**26 + d, 1), far[i].storage_offset()) for i in range(2))
+    q.copy_(s.rand(new, 4 * kvh, "bf16"))
+    cache.attend(1, q, out, s.batch)
+    check_attention(s, kv, q.contiguous(), out.contiguous(), "bf16")
+    k, v = (far[i].as_strided((new, kvh, d), (d, 2**26 + d, 1), far[i].storage_offset()) for i in range(2))
+    cache.read(1, k, v, s.batch)
+    cache.check()
+    for t, x in zip((k, v), kv[0]):
+        assert torch.equal(t.cpu(), torch.from_numpy(x[n_len - new:]).float().bfloat16())
