@@ -17,10 +17,9 @@
 // Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
 // A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
-// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 148 us, 4.8 TB/s,
-// 0.73 of the copy rate; the copies alone take 117, the instructions alone 144 (64-value
-// heads: 24 sequences 57 us for 32 of bytes).  Fewer registers for a fifth CTA on the SM
-// spill and lose (267 us).  Splits along the positions, where rows are few, are joined in
+// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 153 us, 4.6 TB/s,
+// 0.70 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 58 us for 32
+// of bytes).  Fewer registers for a fifth CTA on the SM spill and lose (267 us).  Splits along the positions, where rows are few, are joined in
 // the cluster's shared memory or by a second small kernel.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -58,9 +57,13 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t hsub1024(uint32_t a) {
-  const uint32_t k = 0xE400E400u;  // -1024, -1024
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t k) {
   const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 // Two codes of a word as operands, c and c' of one half each: their bits as they are, the
@@ -71,15 +74,28 @@ __device__ __forceinline__ uint32_t hsub1024(uint32_t a) {
 // 2-norm, one of 16384 1.2e-4).
 template <bool NORMAL>
 __device__ __forceinline__ uint32_t low(uint32_t x) {
-  return NORMAL ? hsub1024((x & 0x000F000Fu) | 0x64006400u) : x & 0x000F000Fu;
+  return NORMAL ? hadd2((x & 0x000F000Fu) | 0x64006400u, 0xE400E400u) : x & 0x000F000Fu;
 }
 template <bool NORMAL>
 __device__ __forceinline__ uint32_t high(uint32_t x) {
-  return NORMAL ? hsub1024((x & 0x00F000F0u) | 0x64006400u) : x & 0x00F000F0u;
+  return NORMAL ? hadd2((x & 0x00F000F0u) | 0x64006400u, 0xE400E400u) : x & 0x00F000F0u;
 }
-// Sums over many positions are kept out of the matrix unit in 32-bit calls: it cuts its
-// sums off instead of rounding them, and the codes' sums all grow in one direction (eight
-// lanes of about 1000 positions: 4e-5 off in the 2-norm with the sums kept there).
+// The same for values: in 32-bit calls (c - 7.5) 2^-9, from the subnormal by one multiply-add,
+// exactly and a normal number whatever c.
+template <bool CENTRE>
+__device__ __forceinline__ uint32_t low_v(uint32_t x) {
+  x &= 0x000F000Fu;
+  return CENTRE ? hfma2(x, 0x78007800u, 0xA380A380u) : x;
+}
+template <bool CENTRE>
+__device__ __forceinline__ uint32_t high_v(uint32_t x) {
+  x &= 0x00F000F0u;
+  return CENTRE ? hfma2(x, 0x68006800u, 0xA380A380u) : x;
+}
+// Sums over more than 16 positions are kept out of the matrix unit: it cuts its sums off
+// instead of rounding them, the codes' sums all grow in one direction, and the minima's part
+// largely takes them back (fp16, 150 sequences of 16384 positions with even weights: results
+// 4.5e-3 off in the 2-norm with the sums kept there, of 131072 4.4e-2).
 __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
   const float2 x = __fadd2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
   const float2 y = __fadd2_rn(make_float2(a[2], a[3]), make_float2(b[2], b[3]));
@@ -134,6 +150,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   // largely cancel, and then see the same weight.  (With one rounding more, fp16 outputs
   // are 5.1e-4 off instead of their own rounding's 2.1e-4; bf16's is 1.7e-3.)
   constexpr bool kExact = kF32 || std::is_same<T, __half>::value;
+  // Values as (z + 7.5 s) + s (c - 7.5): neither part has a mean of its own, so that long sums do
+  // not grow only to cancel (2048 of a tile's products added in 32 bits, 131072 positions: 4e-4 off
+  // in the 2-norm without).  It costs little where codes are made normal numbers anyway: the sum
+  // over a tile of w s is in rows 8..15 of the minima's product, which would be idle.  16-bit calls
+  // bound the sum's length instead (all types so: 64 long sequences 153 -> 170 us).
+  constexpr bool kCentre = kF32;
+  constexpr float kLow = kCentre ? 512.f : 16777216.f, kHigh = kCentre ? 512.f : 1048576.f;  // a value's code over its operand's
   constexpr int MT = kF32 ? NT : (NT + 1) / 2;          // 16-row operands of the queries
   constexpr int kTilesPerStage = kStageBytes / L::kBytes;
   constexpr int kStagePos = kTilesPerStage * kKv4Tile;  // positions of a stage
@@ -305,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   }
 
   // oz: row g the minima's part of group g, row G (operand of ones) the sum of the weights
-  float o[NT][G][2][4], oz[NT][4], m[NT], ref[NT];
+  float o[NT][G][2][4], oz[NT][2], m[NT], ref[NT];
   // weights are scaled by 2^lift: 14 - kHead, or less where scales are large; cap: the
   // largest scale this lift allows (a pair of halves)
   int lift = 14 - kHead;
@@ -315,7 +338,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     m[t] = -INFINITY;
     ref[t] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) oz[t][i] = 0.f;
+    for (int i = 0; i < 2; ++i) oz[t][i] = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -436,7 +459,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
         ref[t] = r;
         const float c0 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig), c1 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig + 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) oz[t][i] *= (i & 1) ? c1 : c0;
+        for (int i = 0; i < 2; ++i) oz[t][i] *= i ? c1 : c0;
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -449,7 +472,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       const uint8_t* tile = tiles + u * L::kBytes;
-      uint32_t vs[2 * G], vz[2];
+      uint32_t vs[2 * G], vz[2], sz[2];  // sz: scales of group gid, as rows 8..15 of the minima's operand
 #pragma unroll
       for (int v = 0; v < 2 * G / 4; ++v) {
         const uint4 y = lds_u4(tile + L::kVs + v * 64 + tig * 16);
@@ -458,11 +481,12 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         vz[n] = gid < G ? lds_u1(tile + L::kVz + gid * 32 + n * 16 + tig * 4) : gid == G ? 0x3C003C00u : 0u;
+        sz[n] = kCentre && gid < G ? lds_u1(tile + L::kVs + (n * G + gid) / 4 * 64 + tig * 16 + (n * G + gid) % 4 * 4) : 0u;
         if constexpr (kMasked) {
           const int p = pos + 16 * u + 8 * n + 2 * tig;
-          vz[n] = finite2(vz[n]);
-          if (p >= p1 && gid < G) vz[n] &= 0xFFFF0000u;
-          if (p + 1 >= p1 && gid < G) vz[n] &= 0xFFFFu;
+          const uint32_t keep = gid >= G ? ~0u : (p < p1 ? 0xFFFFu : 0u) | (p + 1 < p1 ? 0xFFFF0000u : 0u);
+          vz[n] = finite2(vz[n]) & keep;
+          sz[n] = finite2(sz[n]) & keep;
         }
       }
       uint32_t wp[NT][2], wl[NT][2];  // weights of positions 2 tig, 2 tig + 1 (+ 8); low parts
@@ -481,15 +505,15 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
           if constexpr (kF32) split2(w[t][2 * n], w[t][2 * n + 1], wp[t][n], wl[t][n]);
           else wp[t][n] = pack_h(w[t][2 * n], w[t][2 * n + 1]);
         }
-        // (rows 8..15 are not used)
+        float z[4];
         if constexpr (kF32) {
-          float z[4];
-          mma16816_zero(z, vz[0], vz[0], vz[1], vz[1], wl[t][0], wl[t][1]);
-          mma16816(z, vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);
-          add4(oz[t], z);
+          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wl[t][0], wl[t][1]);
+          mma16816(z, vz[0], sz[0], vz[1], sz[1], wp[t][0], wp[t][1]);
         } else {
-          mma16816(oz[t], vz[0], vz[0], vz[1], vz[1], wp[t][0], wp[t][1]);
+          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wp[t][0], wp[t][1]);
         }
+        oz[t][0] += kCentre ? fmaf(7.5f, z[2], z[0]) : z[0];
+        oz[t][1] += kCentre ? fmaf(7.5f, z[3], z[1]) : z[1];
       }
       uint32_t vc[2 * G];
 #pragma unroll
@@ -500,8 +524,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint32_t x0 = vc[2 * g], x1 = vc[2 * g + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-        const uint32_t a0 = low<kF32>(x0), a1 = high<kF32>(x0), a2 = low<kF32>(x1), a3 = high<kF32>(x1);
-        const uint32_t b0 = low<kF32>(y0), b1 = high<kF32>(y0), b2 = low<kF32>(y1), b3 = high<kF32>(y1);
+        const uint32_t a0 = low_v<kCentre>(x0), a1 = high_v<kCentre>(x0), a2 = low_v<kCentre>(x1), a3 = high_v<kCentre>(x1);
+        const uint32_t b0 = low_v<kCentre>(y0), b1 = high_v<kCentre>(y0), b2 = low_v<kCentre>(y1), b3 = high_v<kCentre>(y1);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           uint32_t p[2], q[2];
@@ -518,22 +542,18 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
               if constexpr (kExact) q[n] &= keep;
             }
           }
-          if constexpr (kF32) {
-            float y0[4], y1[4];
+          float y0[4], y1[4];
+          if constexpr (kExact) {
             mma16816_zero(y0, a0, a1, a2, a3, q[0], q[1]);
             mma16816_zero(y1, b0, b1, b2, b3, q[0], q[1]);
             mma16816(y0, a0, a1, a2, a3, p[0], p[1]);
             mma16816(y1, b0, b1, b2, b3, p[0], p[1]);
-            add4(o[t][g][0], y0);
-            add4(o[t][g][1], y1);
           } else {
-            mma16816(o[t][g][0], a0, a1, a2, a3, p[0], p[1]);
-            mma16816(o[t][g][1], b0, b1, b2, b3, p[0], p[1]);
-            if constexpr (kExact) {
-              mma16816(o[t][g][0], a0, a1, a2, a3, q[0], q[1]);
-              mma16816(o[t][g][1], b0, b1, b2, b3, q[0], q[1]);
-            }
+            mma16816_zero(y0, a0, a1, a2, a3, p[0], p[1]);
+            mma16816_zero(y1, b0, b1, b2, b3, p[0], p[1]);
           }
+          add4(o[t][g][0], y0);
+          add4(o[t][g][1], y1);
         }
       }
     }
@@ -587,9 +607,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int j = 0; j < 2; ++j) {
         float* d0 = ob + (warp * kRows + 8 * t + 2 * tig) * D + 32 * g + 4 * gid + 2 * j;
         *reinterpret_cast<float2*>(d0) =
-            make_float2(fmaf(o[t][g][j][0], kCode, z0), fmaf(o[t][g][j][2], kCode / 16.f, z0));
+            make_float2(fmaf(o[t][g][j][0], kLow, z0), fmaf(o[t][g][j][2], kHigh, z0));
         *reinterpret_cast<float2*>(d0 + D) =
-            make_float2(fmaf(o[t][g][j][1], kCode, z1), fmaf(o[t][g][j][3], kCode / 16.f, z1));
+            make_float2(fmaf(o[t][g][j][1], kLow, z1), fmaf(o[t][g][j][3], kHigh, z1));
       }
     }
   }
@@ -818,9 +838,12 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   // and where there are more, up to eight CTAs per SM in pieces of 32 pages, so that
   // sequences of unequal length fill the SMs evenly (64 of up to 16384 positions, kv heads
   // of 128: 190 us unsplit, 146 so; 64 of about 2000 lose by a split, 55 to 65 us).
-  long long n_split = 1;
+  // A sum of 32 bits that a warp keeps over more than 4096 positions shows in 16-bit results, whose
+  // codes' and minima's parts cancel: at most 16384 to a split in any case.
+  const long long least = dtype == 2 ? 1 : std::max(1ll, (pages + 255) / 256);
+  long long n_split = least;
   if (base > 0)
-    n_split = std::max({1ll, std::min(2ll * sms / base, pages / kWarps), std::min(8ll * sms / base, pages / 32)});
+    n_split = std::max({n_split, std::min(2ll * sms / base, pages / kWarps), std::min(8ll * sms / base, pages / 32)});
   // Where the splits fill the SMs about once, up to 16 of them are a cluster (a power of
   // two): no workspace and no second launch (eight lanes of about 1000 positions in fp32:
   // 9.6 -> 8.3 us).  Longer grids lose by it, a cluster's CTAs being placed together (64
@@ -828,7 +851,7 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   p->cluster = n_split > 1 && n_split <= 16 && base * n_split <= 2ll * sms;
   if (p->cluster) {
     long long c = 2;
-    while (2 * c <= std::min(n_split, 16ll)) c *= 2;
+    while (2 * c <= std::min(n_split, 16ll) || c < least) c *= 2;
     n_split = c;
   }
   const long long per = std::max(1ll, (pages + n_split - 1) / n_split);

@@ -1,0 +1,160 @@
+"""The 4-bit KV cache on the GPU where a call can go wrong: long runs, far ranges, batches of very
+unequal sequences, streams, errors (needs a B200)."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _kv4 as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from persistent_megakernel_02_b200 import build
+
+    build.build()
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+class Shared:
+    """One sequence of `n_len` positions in a cache, and `lens` sequences that are its first positions:
+    they read the same pages, so many long sequences cost one."""
+
+    def __init__(self, d, kv_heads, n_len, lens, new=None, make_k=None, make_v=None, seed=0):
+        from persistent_megakernel_02_b200 import Kv4Cache
+
+        self.d, self.kv_heads, self.lens = d, kv_heads, list(lens)
+        self.new = [1] * len(self.lens) if new is None else list(new)
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        pages = -(-n_len // R.PAGE)
+        row = torch.randperm(pages, generator=self.gen, device="cuda").int()
+        self.table = row[None].expand(len(self.lens), pages).contiguous()
+        self.cache = Kv4Cache.empty(1, pages, kv_heads, d, self.table)
+        self.cache.pool.fill_(255)
+        shape = (n_len, kv_heads, d)
+        k, v = (torch.randn(shape, generator=self.gen, device="cuda") for _ in range(2))
+        k, v = k if make_k is None else make_k(k), v if make_v is None else make_v(v)
+        whole = self.cache.batch(ints([0, n_len]), ints([n_len]), n_len, n_len, n_len)
+        self.cache.append(0, k, v, whole)
+        self.cache.read(0, k, v, whole)  # what the cache stands for
+        self.k, self.v = k, v
+        self.cu = np.concatenate([[0], np.cumsum(self.new)])
+        self.rows = int(self.cu[-1])
+        self.batch = self.cache.batch(ints(self.cu), ints(self.lens), self.rows, max(self.new), max(self.lens))
+
+    def queries(self, heads, dtype, size=1.0):
+        return (torch.randn((self.rows, heads, self.d), generator=self.gen, device="cuda") * size).to(R.DTYPES[dtype])
+
+    def attend(self, q, **kw):
+        out = torch.full_like(q, -7.0)
+        self.cache.attend(0, q, out, self.batch, **kw)
+        return out
+
+    def want(self, q, i, k=None, v=None, scale=None):
+        """Rows of sequence i, float64."""
+        k, v = self.k if k is None else k, self.v if v is None else v
+        n, n_len = self.new[i], self.lens[i]
+        x = q[self.cu[i]:self.cu[i + 1]].double()
+        rep = q.shape[1] // self.kv_heads
+        see = torch.arange(n_len, device="cuda")[None] <= torch.arange(n_len - n, n_len, device="cuda")[:, None]
+        out = torch.empty_like(x)
+        for h in range(q.shape[1]):
+            kk, vv = k[:n_len, h // rep].double(), v[:n_len, h // rep].double()
+            s = (x[:, h] @ kk.T * (R.default_scale(self.d) if scale is None else scale)).masked_fill(~see, -np.inf)
+            out[:, h] = torch.softmax(s, -1) @ vv
+        return out
+
+    def got(self, out, i):
+        return out[self.cu[i]:self.cu[i + 1]].double()
+
+
+# Bounds of the 2-norm of the error over that of the result for single tokens and a few.  A rounding
+# to t bits is off by u / m, u evenly spread up to half a step and m the mantissa, 1 to 2: in the mean
+# of squares over a binade 2.1e-4 for fp16 and 1.67e-3 for bf16, and an eighth more for mantissas not
+# spread evenly.
+#   fp16: weights and outputs rounded, V as it is: 3.3e-4.
+#   bf16: outputs rounded, weights and weight * scale to fp16.  The latter's part of a value, s c, is in
+#   the mean of squares 2.3 times the value of normal rows (a group spans 4.1 of their deviations, so
+#   codes stand for 2.05 +- 1 of them): sqrt(1.67^2 + 0.21^2 + 0.48^2) = 1.75e-3, and an eighth: 2.0e-3.
+#   fp32: two fp16 parts of 22 bits, signs varying, a factor of 8 for the parts that cancel: 2^-18.
+NORM = {"fp16": 3.3e-4, "bf16": 2.0e-3, "fp32": 2.0**-18}
+
+
+def norm_error(got, want):
+    return float(torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want))
+
+
+# ---- sums over many positions -----------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d,n_len", [(64, 131072 + 5), (64, 16384 + 37), (128, 65536 + 37), (128, 16384 + 1)])
+def test_many_long_sequences_keep_their_sums(d, n_len, dtype):
+    """So many sequences that nothing splits them but their length: a warp goes over thousands of
+    positions, whose codes' and minima's parts largely cancel, so that a sum that is cut off, or
+    that grows, shows.  Keys are small, as weights spread over many positions make it worst."""
+    n = 150
+    s = Shared(d, 8, n_len, [n_len - 61 * (i % 40) for i in range(n)], make_k=lambda k: k * 0.25)
+    q = s.queries(16, dtype)
+    out = s.attend(q)
+    s.cache.check()
+    for i in (0, 39, n - 1):
+        want, got = s.want(q, i), s.got(out, i)
+        assert norm_error(got, want) < NORM[dtype]
+        # one head's row: 64 or 128 terms, half as much again
+        worst = (torch.linalg.vector_norm(got - want, dim=-1) / torch.linalg.vector_norm(want, dim=-1)).max()
+        assert float(worst) < 1.5 * NORM[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [2, 8])
+def test_a_few_rows_of_many_long_sequences(d, new, dtype):
+    n_len = 9000
+    s = Shared(d, 8, n_len, [n_len - 61 * (i % 40) for i in range(80)], new=[new - i % 2 for i in range(80)],
+               make_k=lambda k: k * 0.25)
+    q = s.queries(32, dtype)
+    out = s.attend(q)
+    s.cache.check()
+    for i in (0, 1, 39):
+        assert norm_error(s.got(out, i), s.want(q, i)) < NORM[dtype]
+
+
+# ---- a whole batch's bounds and a sequence's own ------------------------------------------
+
+
+def mixed(d, kv_heads, lens, new, **kw):
+    return Shared(d, kv_heads, max(lens), lens, new, make_k=lambda k: k * 0.25, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d,kv_heads,lens,new", [
+    (64, 8, [3000, 1500, 70, 2900, 1, 0, 2500] + [2999] * 20, [1500, 1, 3, 1, 1, 0, 700] + [1] * 20),
+    (128, 8, [900] * 30 + [1100], [1] * 30 + [1100]),
+    (64, 2, [5000, 4000, 3000], [65, 3000, 1]),
+    (128, 8, [2000] + [1999] * 40, [1999] + [1] * 40),
+    (64, 1, [40000, 100, 39000], [2049, 1, 300]),
+])
+def test_prompts_and_single_tokens_in_one_call(d, kv_heads, lens, new, dtype):
+    s = mixed(d, kv_heads, lens, new)
+    q = s.queries(4 * kv_heads, dtype)
+    out = s.attend(q)
+    s.cache.check()
+    # rounding K and V in 16-bit prompts adds 2.1e-4 each, an eighth for uneven mantissas; rows that see
+    # few positions, with weights far from even, are of the size of V, so the norm is over all
+    bound = NORM[dtype] if dtype == "fp32" else NORM[dtype] + 2.4e-4
+    for i in range(len(lens)):
+        if new[i] and lens[i]:
+            assert norm_error(s.got(out, i), s.want(q, i)) < bound, i
+    again = s.attend(q)
+    assert torch.equal(out, again)
+    free = s.attend(q, workspace=torch.full((max(16, s.cache.workspace_bytes(s.batch, q.shape[1], q.dtype)),), 255,
+                                            dtype=torch.uint8, device="cuda"))
+    assert torch.equal(out, free)
