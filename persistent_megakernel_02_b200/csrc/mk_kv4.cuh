@@ -108,6 +108,12 @@ __device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, uint32_
   return false;
 }
 
+// What accumulated scores are multiplied by to be in powers of two, kept finite: where it is not
+// (queries beyond 2^100, a scale beyond 1e34) scores that differ at all do so by 2^-72 of the
+// accumulated ones, so that the largest has all the weight with 2^127 too.  Never zero: it
+// multiplies the -inf of masked positions.
+__device__ __forceinline__ float kv4_score_scale(float k) { return fminf(fmaxf(k, 1e-37f), 1.7e38f); }
+
 // ---- rows of 16-bit or 32-bit values ----
 template <class T>
 struct Raw8 {  // 8 values as they are in memory

@@ -11,16 +11,16 @@
 // Values the same way: O = sum_p w_p V_p = sum_g c (w s)_g + z_g w, the weights of a
 // position times its scale are the operand, and one mma holds the z part of all groups.
 // The softmax runs in one pass with a running maximum and sum per row; the operand w s
-// is kept in fp16's range by the running reference, which also counts the power of two
-// of the largest scale met so far.
+// is kept in fp16's range by a power of two that follows the largest scale met so far.
 //
 // Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
 // A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
-// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 153 us, 4.6 TB/s,
-// 0.70 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 58 us for 32
-// of bytes).  Fewer registers for a fifth CTA on the SM spill and lose (267 us).  Splits along the positions, where rows are few, are joined in
-// the cluster's shared memory or by a second small kernel.
+// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 151 us, 4.7 TB/s,
+// 0.71 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 58 us for 32
+// of bytes).  Fewer registers for a fifth CTA on the SM spill and lose (267 us).  Splits along
+// the positions, where rows are few, are joined in the cluster's shared memory or by a second
+// small kernel.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -275,8 +275,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
     const float up = __uint_as_float((uint32_t)(127 + max(e, -126)) << 23);
     const float signed_up = a.scale_log2 < 0.f ? -up : up;
-    // (never zero: it multiplies the -inf of masked positions)
-    kscale[t] = fmaxf(fabsf(a.scale_log2) * kCode / up, 1e-37f);
+    kscale[t] = kv4_score_scale(fabsf(a.scale_log2) / up * kCode);
     lim[t] = live ? start + r / a.rep + 1 : 0;
     float sums[G];
 #pragma unroll
@@ -328,15 +327,18 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   }
 
   // oz: row g the minima's part of group g, row G (operand of ones) the sum of the weights
-  float o[NT][G][2][4], oz[NT][2], m[NT], ref[NT];
-  // weights are scaled by 2^lift: 14 - kHead, or less where scales are large; cap: the
-  // largest scale this lift allows (a pair of halves)
+  float o[NT][G][2][4], oz[NT][2];
+  // Weights are 2^((score - peak) kscale + lift) of the accumulated scores: peak is the row's
+  // largest when it was last moved (0: none so far), which happens when one passes `bound`.
+  // lift: 14 - kHead, or less where scales are large; cap: the largest scale it allows (a pair of
+  // halves).
+  float peak[NT], bound[NT];
   int lift = 14 - kHead;
   uint32_t cap = 0x3FFF3FFFu;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = -INFINITY;
-    ref[t] = 0.f;
+    bound[t] = -INFINITY;
+    peak[t] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) oz[t][i] = 0.f;
 #pragma unroll
@@ -418,9 +420,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
         }
       }
     }
-    // The weights are 2^(score - ref), ref = m - lift with m the row's maximum when it was
-    // last moved: it moves only when a score passes m by more than kHead (or a scale the
-    // largest one allowed so far), so most steps need one vote and no shuffle.
+    // The peak moves only when a score passes it by more than kHead (or a scale the largest
+    // one allowed so far), so most steps need one vote and no shuffle.
     bool over = hmax2(top, cap) != cap;
     float mx[NT];
 #pragma unroll
@@ -439,13 +440,14 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       }
 #pragma unroll
       for (int u = 1; u < SUB; ++u) r[0] = fmaxf(r[0], r[u]);
-      mx[t] = r[0] * kscale[t];
-      over |= mx[t] > m[t] + kHead;
+      mx[t] = r[0];
+      over |= r[0] > bound[t];
     }
     if (__any_sync(0xFFFFFFFFu, over)) {
       top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       top = max(top & 0xFFFFu, top >> 16);
+      const int before = lift;
       lift = min(lift, 29 - kHead - (int)(top >> 10));  // top < 2^(exponent - 14): weight * scale < 2^15
       cap = ((uint32_t)(30 - kHead - lift) << 10) - 1u;
       cap |= cap << 16;
@@ -453,10 +455,12 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int t = 0; t < NT; ++t) {
         mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xFFFFFFFFu, mx[t], 1));
         mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xFFFFFFFFu, mx[t], 2));
-        const bool first = m[t] == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
-        m[t] = fmaxf(m[t], mx[t]);
-        const float r = (m[t] == -INFINITY ? 0.f : m[t]) - (float)lift, corr = first ? 0.f : ex2(ref[t] - r);
-        ref[t] = r;
+        const bool first = bound[t] == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
+        const float now = first ? mx[t] : fmaxf(peak[t], mx[t]);
+        const float b = now == -INFINITY ? 0.f : now;
+        const float corr = first ? 0.f : ex2(fmaf(peak[t] - b, kscale[t], (float)(lift - before)));
+        peak[t] = b;
+        bound[t] = __fadd_rd(now, kHead / kscale[t]);  // (never more than kHead above)
         const float c0 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig), c1 = __shfl_sync(0xFFFFFFFFu, corr, 8 * tig + 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) oz[t][i] *= i ? c1 : c0;
@@ -495,8 +499,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float2 e = __ffma2_rn(make_float2(s[t][u][i], s[t][u][i + 1]), make_float2(kscale[t], kscale[t]),
-                                      make_float2(-ref[t], -ref[t]));
+          // (the difference first: scores far from zero keep their order, and equal ones their weights)
+          const float2 e = __ffma2_rn(__fadd2_rn(make_float2(s[t][u][i], s[t][u][i + 1]), make_float2(-peak[t], -peak[t])),
+                                      make_float2(kscale[t], kscale[t]), make_float2((float)lift, (float)lift));
           w[t][i] = ex2(e.x);
           w[t][i + 1] = ex2(e.y);
         }
@@ -592,9 +597,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   float* ob = reinterpret_cast<float*>(smem);            // [warp][row][D]
   float* ml = ob + kWarps * kRows * D;                   // [warp][row][2]
   float* own = ml + kWarps * kRows * 2;                  // [row][D + 4], of a cluster's CTA
+  // without the lift, which a reference far from zero would swallow
+  const float down = __uint_as_float((uint32_t)(127 - lift) << 23), c_low = kLow * down, c_high = kHigh * down;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if (tig == 0) ml[(warp * kRows + 8 * t + gid) * 2] = ref[t];
+    if (tig == 0) ml[(warp * kRows + 8 * t + gid) * 2] = peak[t] * kscale[t];
+    oz[t][0] *= down;
+    oz[t][1] *= down;
     if (gid == G) {  // the row of ones has the sums of the weights
       ml[(warp * kRows + 8 * t + 2 * tig) * 2 + 1] = oz[t][0];
       ml[(warp * kRows + 8 * t + 2 * tig + 1) * 2 + 1] = oz[t][1];
@@ -607,9 +616,9 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       for (int j = 0; j < 2; ++j) {
         float* d0 = ob + (warp * kRows + 8 * t + 2 * tig) * D + 32 * g + 4 * gid + 2 * j;
         *reinterpret_cast<float2*>(d0) =
-            make_float2(fmaf(o[t][g][j][0], kLow, z0), fmaf(o[t][g][j][2], kHigh, z0));
+            make_float2(fmaf(o[t][g][j][0], c_low, z0), fmaf(o[t][g][j][2], c_high, z0));
         *reinterpret_cast<float2*>(d0 + D) =
-            make_float2(fmaf(o[t][g][j][1], kLow, z1), fmaf(o[t][g][j][3], kHigh, z1));
+            make_float2(fmaf(o[t][g][j][1], c_low, z1), fmaf(o[t][g][j][3], c_high, z1));
       }
     }
   }
@@ -837,7 +846,7 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   // (one sequence of 8200 positions, 8 kv heads of 64: 15.9 us with 4 splits, 9.1 with 32);
   // and where there are more, up to eight CTAs per SM in pieces of 32 pages, so that
   // sequences of unequal length fill the SMs evenly (64 of up to 16384 positions, kv heads
-  // of 128: 190 us unsplit, 146 so; 64 of about 2000 lose by a split, 55 to 65 us).
+  // of 128: 190 us unsplit, 151 so; 64 of about 2000 lose by a split, 55 to 65 us).
   // A sum of 32 bits that a warp keeps over more than 4096 positions shows in 16-bit results, whose
   // codes' and minima's parts cancel: at most 16384 to a split in any case.
   const long long least = dtype == 2 ? 1 : std::max(1ll, (pages + 255) / 256);

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23), sup = a.scale_log2 < 0.f ? -up : up;
       [[maybe_unused]] uint32_t qt[16];
-      kscale = fmaxf(fabsf(a.scale_log2) / up, 1e-37f);  // (never zero: it multiplies the -inf of masked positions)
+      kscale = kv4_score_scale(fabsf(a.scale_log2) / up);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         float x[8];
@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
     const bool whole = row0 + t * kPTile + (r_in | 31) < n_rows;      // no row of the warp is past the end
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = lane_base + (uint32_t)(t * 128), to = lane_base + kO + (uint32_t)(t * D);
-    float m = -INFINITY, ref = 0.f, sum = 0.f;
+    // weights are 2^((score - peak) kscale + kPLift), peak the largest accumulated score when it was
+    // last moved (0: none so far), which happens when one passes `bound`
+    float peak = 0.f, bound = -INFINITY, sum = 0.f;
     const int n = n_half[t];
     bool ok = true;
     for (int i = 0; i < n; ++i) {
@@ -364,15 +366,15 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       tc_fence_after();
       uint32_t s[64];
       tmem_get64(ts + 64 * h, s);
-      const int base = p0 + i * 64, left = lim - base;  // columns with position < left are seen
+      const int pos = p0 + i * 64, left = lim - pos;  // columns with position < left are seen
       const uint32_t bad0 = sh.bad[(i >> 1) & 3][2 * h], bad1 = sh.bad[(i >> 1) & 3][2 * h + 1];
       float mx;
-      if (whole && base + 64 <= lim_warp && (bad0 | bad1) == 0) {
+      if (whole && pos + 64 <= lim_warp && (bad0 | bad1) == 0) {
         float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 64; c += 2)
           q[(c >> 1) & 3] = max3(q[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        mx = fmaxf(max3(q[0], q[1], q[2]), q[3]) * kscale;
+        mx = fmaxf(max3(q[0], q[1], q[2]), q[3]);
       } else {  // (with a maximum of its own: a mask in the common code is paid by every tile)
         mx = -INFINITY;
 #pragma unroll
@@ -380,13 +382,13 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
           if (column_position(c) >= left || (c < 32 ? bad0 : bad1)) s[c] = 0xFF800000u;
           mx = fmaxf(mx, __uint_as_float(s[c]));
         }
-        mx *= kscale;
       }
-      if (__any_sync(0xFFFFFFFFu, mx > m + (float)kPHead)) {  // the reference moves: seldom
-        const bool first = m == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
-        m = fmaxf(m, mx);
-        const float r = (m == -INFINITY ? 0.f : m) - (float)kPLift, corr = first ? 0.f : pex2(ref - r);
-        ref = r;
+      if (__any_sync(0xFFFFFFFFu, mx > bound)) {  // the peak moves: seldom
+        const bool first = bound == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
+        const float now = first ? mx : fmaxf(peak, mx), b = now == -INFINITY ? 0.f : now;
+        const float corr = first ? 0.f : pex2((peak - b) * kscale);
+        peak = b;
+        bound = __fadd_rd(now, kPHead / kscale);  // (never more than kPHead above)
         sum *= corr;
         if (i > 0) {  // O, once the product of the half before is in it
           ok = __all_sync(0xFFFFFFFFu, kv4_wait(&sh.wv_done[t], (i - 1) & 1, a.c.status));
@@ -403,13 +405,14 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
         }
       }
       float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 k2 = make_float2(kscale, kscale), r2 = make_float2(-ref, -ref);
+      const float2 k2 = make_float2(kscale, kscale), b2 = make_float2(-peak, -peak), lift2 = make_float2(kPLift, kPLift);
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), k2, r2);
+          // (the difference first: scores far from zero keep their order, and equal ones their weights)
+          float2 x = __ffma2_rn(__fadd2_rn(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), b2), k2, lift2);
           x.x = pex2(x.x);
           x.y = pex2(x.y);
           part[(c >> 1) & 1] = __fadd2_rn(part[(c >> 1) & 1], x);
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       const float inv = sum == 0.f ? 0.f : a.n_split > 1 ? 1.0f : 1.0f / sum;  // 0: the row sees nothing
       const size_t tile = (size_t)(si * a.c.n_kv_heads + head) * a.n_rt + (a.n_rt - 1 - blk);
       float* part = a.part + ((tile * a.n_split + split) * (2 * kPTile) + t * kPTile + r_in) * (D + 4);
-      if (a.n_split > 1 && live) *reinterpret_cast<float2*>(part) = make_float2(sum == 0.f ? -INFINITY : ref, sum);
+      if (a.n_split > 1 && live) *reinterpret_cast<float2*>(part) = make_float2(sum == 0.f ? -INFINITY : peak * kscale, sum);
       char* dst = a.out + (long long)(seq.row0 + row / a.rep) * a.o_row +
                   (long long)(head * a.rep + row % a.rep) * a.o_head;
 #pragma unroll

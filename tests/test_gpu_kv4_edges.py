@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import _kv4 as R
+from tests.test_gpu_kv4 import Setup
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +159,55 @@ def test_prompts_and_single_tokens_in_one_call(d, kv_heads, lens, new, dtype):
     free = s.attend(q, workspace=torch.full((max(16, s.cache.workspace_bytes(s.batch, q.shape[1], q.dtype)),), 255,
                                             dtype=torch.uint8, device="cuda"))
     assert torch.equal(out, free)
+
+
+# ---- far ranges --------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("new", [1, 300])
+@pytest.mark.parametrize("d,kv_heads", [(64, 16), (128, 16)])
+@pytest.mark.parametrize("dtype,q_size,scale", [
+    ("bf16", 2.0**20, None), ("bf16", 2.0**23, None), ("bf16", 2.0**27, None), ("bf16", 2.0**60, None), ("bf16", 2.0**119, None),
+    ("bf16", -(2.0**119), None), ("bf16", 1.0, 1e34), ("bf16", 1.0, -1e34), ("fp16", 1.0, 1e34), ("fp16", 40000.0, 2.0**10),
+    ("fp32", 2.0**22, None), ("fp32", 2.0**27, None), ("fp32", 2.0**119, None), ("fp32", 1.0, 1e34),
+])
+def test_scores_far_from_each_other(dtype, q_size, scale, d, kv_heads, new):
+    """Two positions with the same key far above the rest, all rows behind them: their mean, however
+    large the finite scores are."""
+    s = Setup(d, kv_heads, [900], [new])
+    sign = torch.from_numpy(np.where(s.rng.random((1, kv_heads, d)) < 0.5, -1.0, 1.0)).float().cuda()
+    up = sign if q_size * (1.0 if scale is None else scale) > 0 else -sign
+    k, v = 0.1 * s.rand(900, kv_heads), s.rand(900, kv_heads)
+    k[[5, 133]] = up * 2.0 * 64 / d
+    s.cache.append(0, k, v, s.full_batch())
+    v = torch.from_numpy(R.quantised(v.double().cpu().numpy()))
+    q = (abs(q_size) * sign.repeat_interleave(2, 1).double() * (1 + 0.1 * torch.rand((new, 2 * kv_heads, d), device="cuda")))
+    q = (q if q_size > 0 else -q).to(R.DTYPES[dtype])
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, out, s.batch, scale=scale)
+    s.cache.check()
+    want = ((v[5] + v[133]) / 2).repeat_interleave(2, 0)[None].numpy()
+    err = np.abs(out.double().cpu().numpy() - want)
+    # V, or weight and weight * scale, to fp16, and the output
+    eps = torch.finfo(R.DTYPES[dtype]).eps / 2
+    assert (err <= eps * np.abs(want) + np.abs(v.numpy()).max() * (2.0**-20 if dtype == "fp32" else 2.0**-10) + 2.0**-24).all()
+
+
+@pytest.mark.parametrize("new", [1, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("q_size", [2.0**20, 2.0**25, 2.0**27, 2.0**90, 2.0**119])
+def test_equal_scores_far_from_zero(q_size, dtype, new):
+    """Keys that are all alike: the mean of the values, whatever the sign and size of the scores."""
+    s = Setup(64, 16, [700], [new])
+    k, v = s.rand(1, 16).expand(700, 16, 64), s.rand(700, 16)
+    s.cache.append(0, k, v, s.full_batch())
+    kv = [tuple(R.quantised(x.double().cpu().numpy()) for x in (k, v))]
+    q = (s.rand(new, 32) * q_size).to(R.DTYPES[dtype])
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, out, s.batch)
+    total = np.cumsum(kv[0][1], 0)
+    see = np.arange(700 - new, 700)
+    want = np.repeat(total[see] / (see + 1)[:, None, None], 2, 1)
+    err = np.abs(out.double().cpu().numpy() - want)
+    tol = R.tolerance(want, np.zeros(want.shape[:2]), np.abs(kv[0][1]).max(), dtype)
+    assert (err <= tol).all(), f"{(err / tol).max()}"
