@@ -16,8 +16,8 @@
 // Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
 // A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
-// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 151 us, 4.7 TB/s,
-// 0.71 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 58 us for 32
+// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 150 us, 4.7 TB/s,
+// 0.71 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 59 us for 32
 // of bytes).  Fewer registers for a fifth CTA on the SM spill and lose (267 us).  Splits along
 // the positions, where rows are few, are joined in the cluster's shared memory or by a second
 // small kernel.
@@ -331,10 +331,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   // Weights are 2^((score - peak) kscale + lift) of the accumulated scores: peak is the row's
   // largest when it was last moved (0: none so far), which happens when one passes `bound`.
   // lift: 14 - kHead, or less where scales are large; cap: the largest scale it allows (a pair of
-  // halves).
+  // halves).  Where all scales so far are below 2^-9, small weights times small scales would
+  // leave fp16's range: the tiles' scales are made 2^boost as large in shared memory (below 2), at
+  // every step, for which cap is 0.
   float peak[NT], bound[NT];
-  int lift = 14 - kHead;
-  uint32_t cap = 0x3FFF3FFFu;
+  int lift = 14 - kHead, boost = 15;
+  uint32_t cap = 0u;
+  [[maybe_unused]] float middle = 7.5f;  // ... of a group, in steps of the scales as they are taken
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     bound[t] = -INFINITY;
@@ -447,10 +450,23 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
       top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = hmax2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       top = max(top & 0xFFFFu, top >> 16);
-      const int before = lift;
-      lift = min(lift, 29 - kHead - (int)(top >> 10));  // top < 2^(exponent - 14): weight * scale < 2^15
-      cap = ((uint32_t)(30 - kHead - lift) << 10) - 1u;
-      cap |= cap << 16;
+      const int before = lift, exponent = (int)(top >> 10), boosted = boost;  // top < 2^(exponent - 14)
+      lift = min(lift, 29 - kHead - exponent);  // weight * scale < 2^15
+      boost = min(boost, exponent < 6 ? 15 - exponent : 0);
+      const float less = __uint_as_float((uint32_t)(127 + boost - boosted) << 23);
+      cap = boost > 0 ? 0u : (((uint32_t)(30 - kHead - lift) << 10) - 1u) * 0x00010001u;
+      if (boost > 0) {
+        if constexpr (kCentre) middle = 7.5f * __uint_as_float((uint32_t)(127 - boost) << 23);
+#pragma unroll 1
+        for (int e = lane; e < SUB * D / 4; e += 32) {  // D bytes of scales a tile
+          const uint32_t at = smem_u32(tiles) + e / (D / 4) * L::kBytes + L::kVs + e % (D / 4) * 4;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hmul2(lds32(at), (uint32_t)(15 + boost) * 0x04000400u)));
+        }
+        fence_proxy_async_smem();  // (the next copy into these bytes comes behind)
+        __syncwarp();
+      } else if constexpr (kCentre) {
+        middle = 7.5f;
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mx[t] = fmaxf(mx[t], __shfl_xor_sync(0xFFFFFFFFu, mx[t], 1));
@@ -469,7 +485,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][g][j][i] *= (i & 1) ? c1 : c0;
+            for (int i = 0; i < 4; ++i) o[t][g][j][i] *= ((i & 1) ? c1 : c0) * less;
       }
     }
     // weights and values
@@ -517,8 +533,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
         } else {
           mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wp[t][0], wp[t][1]);
         }
-        oz[t][0] += kCentre ? fmaf(7.5f, z[2], z[0]) : z[0];
-        oz[t][1] += kCentre ? fmaf(7.5f, z[3], z[1]) : z[1];
+        oz[t][0] += kCentre ? fmaf(middle, z[2], z[0]) : z[0];
+        oz[t][1] += kCentre ? fmaf(middle, z[3], z[1]) : z[1];
       }
       uint32_t vc[2 * G];
 #pragma unroll
@@ -598,7 +614,8 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   float* ml = ob + kWarps * kRows * D;                   // [warp][row][2]
   float* own = ml + kWarps * kRows * 2;                  // [row][D + 4], of a cluster's CTA
   // without the lift, which a reference far from zero would swallow
-  const float down = __uint_as_float((uint32_t)(127 - lift) << 23), c_low = kLow * down, c_high = kHigh * down;
+  const float down = __uint_as_float((uint32_t)(127 - lift) << 23), unboost = __uint_as_float((uint32_t)(127 - boost) << 23),
+              c_low = kLow * down * unboost, c_high = kHigh * down * unboost;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     if (tig == 0) ml[(warp * kRows + 8 * t + gid) * 2] = peak[t] * kscale[t];
@@ -846,7 +863,7 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   // (one sequence of 8200 positions, 8 kv heads of 64: 15.9 us with 4 splits, 9.1 with 32);
   // and where there are more, up to eight CTAs per SM in pieces of 32 pages, so that
   // sequences of unequal length fill the SMs evenly (64 of up to 16384 positions, kv heads
-  // of 128: 190 us unsplit, 151 so; 64 of about 2000 lose by a split, 55 to 65 us).
+  // of 128: 190 us unsplit, 150 so; 64 of about 2000 lose by a split, 55 to 65 us).
   // A sum of 32 bits that a warp keeps over more than 4096 positions shows in 16-bit results, whose
   // codes' and minima's parts cancel: at most 16384 to a split in any case.
   const long long least = dtype == 2 ? 1 : std::max(1ll, (pages + 255) / 256);

@@ -211,3 +211,32 @@ def test_equal_scores_far_from_zero(q_size, dtype, new):
     err = np.abs(out.double().cpu().numpy() - want)
     tol = R.tolerance(want, np.zeros(want.shape[:2]), np.abs(kv[0][1]).max(), dtype)
     assert (err <= tol).all(), f"{(err / tol).max()}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("v_size", [2.0**-20, 2.0**-17, 2.0**-13, 2.0**-9, 1.0, 2.0**12])
+@pytest.mark.parametrize("grow", [False, True])
+def test_small_values_under_uneven_weights(v_size, d, dtype, grow):
+    """Values whose scales are fp16's smallest, and a position in 200 with 2^12 times the others' weight:
+    the others together still count.  `grow`: values 2^10 times as large come up later on."""
+    n_len = 9000
+    at = torch.rand(n_len, generator=torch.Generator("cuda").manual_seed(1), device="cuda") < 1 / 200
+
+    def keys(k):
+        k = torch.zeros_like(k)
+        k[at] = 12.0 * np.log(2) / np.sqrt(d)  # with queries of ones: 12 in the exponent of 2
+        return k
+
+    def values(v):
+        v = v * v_size
+        if grow:
+            v[5000:] *= min(2.0**10, 2.0**12 / v_size)
+        return v
+
+    s = Shared(d, 8, n_len, [4000 + 40 * (i % 120) for i in range(150)], make_k=keys, make_v=values)
+    q = torch.ones((s.rows, 16, d), device="cuda").to(R.DTYPES[dtype])
+    out = s.attend(q)
+    s.cache.check()
+    for i in (0, 24, 26, 119):
+        assert norm_error(s.got(out, i), s.want(q, i)) < NORM[dtype], i
