@@ -356,11 +356,13 @@ mk_status mk_matvec_engine_status(void* stream);
  * positions, and per batch a table of each sequence's pages.  Sequence lengths live
  * on the device, so a captured graph can be replayed while they grow; the host gives
  * their bounds.  A batch with numbers outside these bounds (cu not ascending
- * within 0 .. n_rows, a span above max_new, a length below 0 or above max_len) or a page
- * id outside the pool is recorded in the cache's status word; the sequence or page it
- * concerns is neither written nor read.  Sequences may share pages that are only
- * read; calls that overlap on the GPU, and the sequences of one call, must not write
- * the same positions, nor may a call read what another writes meanwhile. */
+ * within 0 .. n_rows, a span above max_new, a length below 0 or above max_len, and for rows
+ * that are written or read back a span above its length) or a page id outside the pool is
+ * recorded in the cache's status word; the sequence or page it concerns is neither written
+ * nor read.  (Where cu does not ascend, append and read may leave out further sequences,
+ * each as a whole.)  Sequences may share pages that are only read; calls that overlap on the
+ * GPU, and the sequences of one call, must not write the same positions, nor may a call read
+ * what another writes meanwhile. */
 #define MK_KV4_PAGE 64
 
 typedef struct {

@@ -52,15 +52,11 @@ struct TileJob {
 // grid of n_rows / 16 + 2 n_seqs slots covers any batch.
 __device__ __forceinline__ TileJob tile_job(const mk_kv4_cache& c, const mk_kv4_batch& b, int layer, int slot) {
   TileJob j{};
-  int lo = 0, hi = b.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.cu[mid] / kKv4Tile + 2 * mid <= slot) lo = mid;
-    else hi = mid - 1;
-  }
+  const int owner = kv4_owner(b, slot, 4, 2), lo = max(owner, 0);
+  static_assert(kKv4Tile == 1 << 4, "");
   const Kv4Seq s = kv4_seq(b, lo);
   const int start = s.len - s.n;
-  if (!s.ok || start < 0) {
+  if (owner < 0 || !s.ok || start < 0) {
     if ((threadIdx.x & 31) == 0) atomicOr(c.status, KV4_BAD_BATCH);
     return j;
   }
@@ -243,6 +239,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
   const int head = (int)(g % c.n_kv_heads), part = (int)(g / c.n_kv_heads % kParts);
   const int slot = (int)(g / (c.n_kv_heads * kParts));
   if (slot >= n_slots) return;
+  if ((threadIdx.x & 31) == 0) kv4_report_order(c, b, g);  // (two slots or more to a sequence)
   const TileJob j = tile_job(c, b, layer, slot);
   if (j.ok) do_tile<D, T, WRITE>(c, j, rows, head, part);
 }

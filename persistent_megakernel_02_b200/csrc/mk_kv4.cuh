@@ -76,6 +76,33 @@ __device__ __forceinline__ Kv4Seq kv4_seq(const mk_kv4_batch& b, int i) {
   return s;
 }
 
+// The sequence that owns slot `slot`, where sequence i owns the slots from (cu[i] >> shift) + extra i up to
+// the next one's first (the caller sees whether the slot is before the first sequence's or behind the
+// last one's).  A warp looks at 32 sequences at a time, every lane calls.  -1 where cu does not ascend in
+// such a way that some slot of that sequence would lead elsewhere: all of the `cu` looked at are on the
+// right side of the sequence's own, so every slot of it takes the same way, and of two sequences that
+// are found none has rows of the other.  (kv4_report_order tells of every cu that does not ascend.)
+__device__ __forceinline__ int kv4_owner(const mk_kv4_batch& b, int slot, int shift, int extra) {
+  if (b.n_seqs == 1) return 0;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = b.n_seqs, below = -0x7FFFFFFF - 1, above = 0x7FFFFFFF;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const int c = at < n ? b.cu[lo + at] : 0x7FFFFFFF;
+    const bool left = lane == 0 || (at < n && (c >> shift) + extra * (lo + at) <= slot);
+    const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, left));
+    if (lane <= k) below = max(below, c);
+    else above = min(above, c);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return __all_sync(0xFFFFFFFFu, below <= b.cu[lo] && above >= b.cu[lo + 1]) ? lo : -1;
+}
+// Thread `i` of a call with at least n_seqs of them looks at one pair.  (A sequence alone is looked at in any case.)
+__device__ __forceinline__ void kv4_report_order(const mk_kv4_cache& c, const mk_kv4_batch& b, long long i) {
+  if (b.n_seqs > 1 && i < b.n_seqs && b.cu[i + 1] < b.cu[i]) atomicOr(c.status, KV4_BAD_BATCH);
+}
+
 // Tile `tile` of a sequence's kv head in a layer, or null for a page id out of range.
 template <int D>
 __device__ __forceinline__ uint8_t* kv4_tile(const mk_kv4_cache& c, const int32_t* table_row, int layer, int head,

@@ -161,6 +161,75 @@ def test_prompts_and_single_tokens_in_one_call(d, kv_heads, lens, new, dtype):
     assert torch.equal(out, free)
 
 
+@pytest.mark.parametrize("cu", [[0, 64, 0, 64], [0, 70, 30, 64], [0, 40, 10, 64], [64, 0, 64, 64], [0, 16, 17, 5],
+                                [0, 64, 64, 0], [0, 10, 5, 5]])
+@pytest.mark.parametrize("call", ["append", "read", "attend", "prompt"])
+def test_a_cu_that_does_not_ascend_is_reported(cu, call):
+    """... and a sequence is served as a whole or not at all; no two that are served share rows."""
+    from persistent_megakernel_02_b200 import MkError
+
+    s = Setup(64, 16, [200, 200, 200], [64, 64, 64])
+    kv = s.fill()
+    s.batch = s.cache.batch(ints(cu), s.kv_lens, 64, 64, 200)
+    k, v = (s.rand(64, 16, "fp32") for _ in range(2))
+    before = s.pool()
+    if call == "append":
+        s.cache.append(0, k, v, s.batch)
+    elif call == "read":
+        k.fill_(-7.0), v.fill_(-7.0)
+        s.cache.read(0, k, v, s.batch)
+    else:
+        q = s.rand(64, 64, "fp32" if call == "attend" else "bf16")
+        out = torch.full_like(q, -7.0)
+        s.cache.attend(0, q, out, s.batch)
+        assert torch.isfinite(out).all()
+    with pytest.raises(MkError, match="batch numbers"):
+        s.cache.check()
+    s.cache.check()
+    if call not in ("append", "read"):
+        return
+    after, taken = s.pool(), np.zeros(64, bool)
+    for i in range(3):
+        a, b = cu[i], cu[i + 1]
+        got = R.unpack(after, 0, s.pages(i), 200)
+        span = slice(200 - (b - a), 200) if b > a else slice(0, 0)
+        if call == "append":
+            if np.array_equal(after[:, s.pages(i)], before[:, s.pages(i)]):
+                continue
+            want = [x.copy() for x in kv[i]]
+            for w, t in zip(want, (k, v)):
+                w[span] = R.quantised(t[a:b].double().cpu().numpy())
+            assert all(np.array_equal(w, g) for w, g in zip(want, got)), i
+        else:
+            rows = [x[span].astype(np.float32) for x in kv[i]]
+            hit = [np.array_equal(t[a:b].cpu().numpy(), r) for t, r in zip((k, v), rows)] if b > a else [False]
+            if not all(hit):
+                continue
+        assert 0 <= a < b <= 64 and not taken[a:b].any(), i
+        taken[a:b] = True
+    if call == "read":  # nothing else was written
+        for t in (k, v):
+            assert (t.cpu().numpy()[~taken] == -7.0).all()
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 1000, 1025, 5000])
+def test_batches_of_many_sequences(n):
+    """Short sequences, some of them empty: every row finds its own."""
+    rng = np.random.default_rng(n)
+    new = rng.choice([0, 0, 1, 1, 2, 17, 33], n).tolist()
+    lens = [v + int(x) for v, x in zip(new, rng.integers(0, 20, n))]
+    s = Setup(64, 1, lens, new, pad_rows=5)
+    k, v = s.rand(s.rows, 1, "bf16"), s.rand(s.rows, 1, "bf16")
+    s.cache.append(0, k, v, s.batch)
+    ko, vo = (torch.full_like(k, -7.0) for _ in range(2))
+    s.cache.read(0, ko, vo, s.batch)
+    s.cache.check()
+    end = s.cu_np[-1]
+    for t, o in ((k, ko), (v, vo)):
+        want = torch.from_numpy(R.quantised(t[:end].double().cpu().numpy())).float().bfloat16()
+        assert torch.equal(o[:end].cpu(), want) and (o[end:] == -7.0).all()
+
+
 # ---- far ranges --------------------------------------------------------------------------
 
 
