@@ -21,6 +21,7 @@
 
 #include "../../include/mk.h"
 #include "mk_device.cuh"
+#include "mk_kv4.h"
 
 namespace mk {
 
@@ -101,6 +102,26 @@ __device__ __forceinline__ int kv4_owner(const mk_kv4_batch& b, int slot, int sh
 // Thread `i` of a call with at least n_seqs of them looks at one pair.  (A sequence alone is looked at in any case.)
 __device__ __forceinline__ void kv4_report_order(const mk_kv4_cache& c, const mk_kv4_batch& b, long long i) {
   if (b.n_seqs > 1 && i < b.n_seqs && b.cu[i + 1] < b.cu[i]) atomicOr(c.status, KV4_BAD_BATCH);
+}
+
+// The row tile of a prompt's CTA, `idx` counting them without the splits; those that see most of
+// their sequence come first.  Every lane calls.
+struct Kv4Block {
+  int seq, head, tile;  // seq -1: a cu that does not ascend; tile: may be none of the sequence's
+};
+__device__ __forceinline__ Kv4Block kv4_block(const Kv4AttnSplit& a, int idx) {
+  Kv4Block r;
+  if (a.n_blocks == 0) {
+    r.tile = a.n_rt - 1 - idx / (a.c.n_kv_heads * a.b.n_seqs);
+    idx %= a.c.n_kv_heads * a.b.n_seqs;
+    r.seq = idx / a.c.n_kv_heads;
+  } else {
+    const int slot = a.n_blocks - 1 - idx / a.c.n_kv_heads;
+    r.seq = kv4_owner(a.b, slot, a.row_shift, 1);
+    r.tile = r.seq < 0 ? -1 : slot - (a.b.cu[r.seq] >> a.row_shift) - r.seq;
+  }
+  r.head = idx % a.c.n_kv_heads;
+  return r;
 }
 
 // Tile `tile` of a sequence's kv head in a layer, or null for a page id out of range.

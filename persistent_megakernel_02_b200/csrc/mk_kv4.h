@@ -31,8 +31,11 @@ struct Kv4Attn {
 // [reference, sum of the weights, -, -, D sums], in fp32.
 struct Kv4AttnSplit : Kv4Attn {
   int n_split, split_len;  // splits of the positions, and positions of each (a multiple of a page, of 128 for prompts)
-  int n_rt;                // row tiles
-  float* part;             // [seq][kv head][row tile, the last first][split][rows of a tile][D + 4]
+  int n_rt;                // row tiles of a sequence
+  // prompts of unequal sequences: row tiles of the whole batch, sequence i's from
+  // (cu[i] >> row_shift) + i on; 0: n_rt to each
+  int n_blocks, row_shift;
+  float* part;             // [CTA of the grid: row tile, then split][rows of a tile][D + 4]
 };
 
 // Opt-in to more than 48 KiB of shared memory (and to clusters of more than 8 CTAs), once

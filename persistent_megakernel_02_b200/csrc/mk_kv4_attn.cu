@@ -765,16 +765,16 @@ template <int D, class T>
 __global__ void __launch_bounds__(128) attn_join_prompt(const AttnArgs a) {
   constexpr int kRows = kKv4PromptRows, kPer = D / 8, kStep = 128 / kPer, kCtas = kRows / kStep;
   const int w8 = threadIdx.x % kPer, r = blockIdx.x % kCtas * kStep + threadIdx.x / kPer, tile = blockIdx.x / kCtas;
-  int idx = tile;
-  const int rt = a.n_rt - 1 - idx % a.n_rt;
-  idx /= a.n_rt;
-  const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
-  const Kv4Seq seq = kv4_seq(a.b, si);
-  const int n_rows = seq.n * a.rep, row0 = rt * kRows, last_row = min(n_rows, row0 + kRows) - 1, row = row0 + r;
+  const Kv4Block block = kv4_block(a, tile);
+  const int head = block.head;
+  const Kv4Seq seq = kv4_seq(a.b, max(block.seq, 0));
+  const int n_rows = seq.n * a.rep;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (block.seq < 0 || !seq.ok || block.tile < 0 || block.tile >= (n_rows + kRows - 1) / kRows) return;
+  const int row0 = block.tile * kRows, last_row = min(n_rows, row0 + kRows) - 1, row = row0 + r;
   const int see_any = max(0, seq.len - seq.n + last_row / a.rep + 1);
   const int n = max(1, min(a.n_split, (see_any + a.split_len - 1) / a.split_len));
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!seq.ok || row > last_row) return;
+  if (row > last_row) return;
   const float* part = a.part + ((size_t)tile * a.n_split * kRows + r) * (D + 4);
   const size_t stride = (size_t)kRows * (D + 4);
   float top = -INFINITY, sum = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -799,6 +799,7 @@ __global__ void __launch_bounds__(128) attn_join_prompt(const AttnArgs a) {
 struct Plan {
   bool prompt;  // many rows of 16-bit queries: the tcgen05 kernel
   int nt, n_rt, n_split, split_len;
+  int n_blocks, row_shift;  // see Kv4AttnSplit
   bool cluster;  // the splits of a row tile are a cluster and join in shared memory
   long long ctas;
   int64_t part_bytes;
@@ -826,29 +827,43 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   // 16 rows x 16 positions take 0.00033 / 0.00062 of the whole GPU, and a call 10 more.  E.g.
   // 8 kv heads x 4 query heads over 16384 positions, 64 values: 16 new tokens 24 here, 27
   // there; 128 tokens 106 here, 243 there unsplit, 45 split; 512 tokens 334, 248, 134.
-  const long long seq_heads = (long long)b->n_seqs * c->n_kv_heads;
+  // Sequences of unequal spans: a batch of n_rows rows has at most n_rows * rep / 256 + n_seqs row tiles,
+  // by which the times go.  Where that is less than half of what it is with as many for every sequence
+  // as for the longest, so do the grid and the workspace (64 sequences, one of 8192 new tokens, 131072
+  // positions: 35 GB without, 0.8).  Looking for a tile's sequence takes longer than an idle CTA: eight
+  // prompts of 517 to 1420 tokens, 129 tiles of 184, 187 us so, 195 by the batch's.
+  const long long seq_heads = (long long)b->n_seqs * c->n_kv_heads, all_rows = (long long)b->n_rows * rep;
+  const auto row_tiles = [&](long long of) { return std::min(b->n_seqs * ((rows + of - 1) / of), all_rows / of + b->n_seqs); };
   p->prompt = false;
+  p->n_blocks = p->row_shift = 0;
   if (dtype != 2 && rows > 16) {
     const bool wide = c->head_dim == 128;
-    const long long n_blocks = (rows + kKv4PromptRows - 1) / kKv4PromptRows, base = n_blocks * seq_heads;
+    const long long n_rt = (rows + kKv4PromptRows - 1) / kKv4PromptRows, blocks = row_tiles(kKv4PromptRows);
+    const bool packed = 2 * blocks < n_rt * b->n_seqs;
+    const long long base = blocks * c->n_kv_heads, grid = packed ? base : n_rt * seq_heads;
     const long long tiles = (b->max_len + 127) / 128;
     // splits of at least four tiles, as many as keep one CTA per SM; and of at most 256, since
     // sums in tensor memory are cut off, not rounded: 0.7e-8 a position, measured (131072
     // positions in one split: results 9e-4 too small)
     const long long n_split = std::max({1ll, std::min(sms / std::max(base, 1ll), tiles / 4), (tiles + 255) / 256});
     const long long per = std::max(1ll, (tiles + n_split - 1) / n_split);
-    const double here = 10 + (double)seq_heads * ((rows + 15) / 16) * ((b->max_len + 15) / 16) * (wide ? 0.00062 : 0.00033);
+    const double here = 10 + (double)c->n_kv_heads * row_tiles(16) * ((b->max_len + 15) / 16) * (wide ? 0.00062 : 0.00033);
     const double tile = dtype == 0 ? (wide ? 2.2 : 1.85) : wide ? 2.75 : 2.15;
     const double there = (double)((base * n_split + sms - 1) / sms) * (6 + per * tile) + (n_split > 1 ? 5 + 0.35 * n_split : 0);
     if (there < here) {
       p->prompt = true;
       p->cluster = false;
       p->nt = 0;
-      p->n_rt = (int)n_blocks;
+      p->n_rt = (int)n_rt;
+      if (packed) {
+        p->n_blocks = (int)blocks;
+        for (p->row_shift = 8; kKv4PromptRows >> p->row_shift < rep;) --p->row_shift;  // 256 / rep rows
+      }
       p->n_split = (int)((tiles + per - 1) / std::max(per, 1ll));
       if (p->n_split < 1) p->n_split = 1;
       p->split_len = (int)std::min<long long>(per * 128, 0x7FFFFF80);
-      p->ctas = base * p->n_split;
+      p->ctas = grid * p->n_split;
+      static_assert(kKv4PromptRows == 1 << 8, "");
       if (p->ctas > 0x7FFFFFFF / kKv4PromptRows) return MK_ERR_UNSUPPORTED;
       p->part_bytes = p->n_split > 1 ? p->ctas * kKv4PromptRows * (c->head_dim + 4) * (int64_t)sizeof(float) : 0;
       return MK_OK;
@@ -1002,7 +1017,7 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
   const AttnArgs a{{*cache, *batch, static_cast<const char*>(q->p), static_cast<char*>(out->p), q->row_stride * size,
               q->head_stride * size, out->row_stride * size, out->head_stride * size, layer, rep,
               scale * 1.44269504088896341f},
-             p.n_split, p.split_len, p.n_rt, static_cast<float*>(workspace)};
+             p.n_split, p.split_len, p.n_rt, p.n_blocks, p.row_shift, static_cast<float*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.prompt) {
     st = kv4_prompt(a, dtype, s);

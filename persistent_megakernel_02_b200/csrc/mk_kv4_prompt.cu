@@ -240,19 +240,18 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
   uint8_t* skv = smem + M::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  int idx = blockIdx.x;
-  const int split = idx % a.n_split;
-  idx /= a.n_split;
-  const int blk = a.n_rt - 1 - idx / (a.c.n_kv_heads * a.b.n_seqs);  // the blocks that see most come first
-  idx %= a.c.n_kv_heads * a.b.n_seqs;
-  const int head = idx % a.c.n_kv_heads, si = idx / a.c.n_kv_heads;
+  const int split = blockIdx.x % a.n_split;
+  const Kv4Block block = kv4_block(a, blockIdx.x / a.n_split);
+  if (a.n_blocks && tid == 0) kv4_report_order(a.c, a.b, blockIdx.x);  // (a row tile or more to a sequence)
+  const int head = block.head, si = max(block.seq, 0);
   const Kv4Seq seq = kv4_seq(a.b, si);
-  if (!seq.ok) {
+  if (block.seq < 0 || !seq.ok) {
     if (tid == 0) atomicOr(a.c.status, KV4_BAD_BATCH);
     return;
   }
-  const int n_rows = seq.n * a.rep, row0 = blk * 2 * kPTile;
-  if (row0 >= n_rows) return;
+  const int n_rows = seq.n * a.rep;
+  if (block.tile < 0 || block.tile >= (n_rows + 2 * kPTile - 1) / (2 * kPTile)) return;
+  const int row0 = block.tile * 2 * kPTile;
   const int start = seq.len - seq.n;  // position of the first query token (may be negative)
   const int p0 = split * a.split_len;  // this split's positions: p0 .. p0 + split_len - 1
   int n_half[2], n_max = 0;            // halves of 64 positions each query tile sees of them; tiles of 128
@@ -433,8 +432,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       tc_fence_after();
       // splits are joined later: the sums as they are, after the reference and the weights' sum
       const float inv = sum == 0.f ? 0.f : a.n_split > 1 ? 1.0f : 1.0f / sum;  // 0: the row sees nothing
-      const size_t tile = (size_t)(si * a.c.n_kv_heads + head) * a.n_rt + (a.n_rt - 1 - blk);
-      float* part = a.part + ((tile * a.n_split + split) * (2 * kPTile) + t * kPTile + r_in) * (D + 4);
+      float* part = a.part + ((size_t)blockIdx.x * (2 * kPTile) + t * kPTile + r_in) * (D + 4);
       if (a.n_split > 1 && live) *reinterpret_cast<float2*>(part) = make_float2(sum == 0.f ? -INFINITY : peak * kscale, sum);
       char* dst = a.out + (long long)(seq.row0 + row / a.rep) * a.o_row +
                   (long long)(head * a.rep + row % a.rep) * a.o_head;
@@ -749,7 +747,7 @@ static mk_status launch(const Kv4AttnSplit& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};
   constexpr int kSmem = PSmem<D, T>::kBytes;
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_prompt<D, T>), kSmem, &ready)) return MK_ERR_CUDA;
-  const long long ctas = (long long)a.n_rt * a.c.n_kv_heads * a.b.n_seqs * a.n_split;
+  const long long ctas = (a.n_blocks ? a.n_blocks : (long long)a.n_rt * a.b.n_seqs) * a.c.n_kv_heads * a.n_split;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
   attn_prompt<D, T><<<(unsigned)ctas, kPThreads, kSmem, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;

@@ -135,6 +135,22 @@ def mixed(d, kv_heads, lens, new, **kw):
     return Shared(d, kv_heads, max(lens), lens, new, make_k=lambda k: k * 0.25, **kw)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_the_workspace_of_a_mixed_batch_is_that_of_its_rows(dtype):
+    """One long prompt beside single tokens, over caches long enough to be split."""
+    from persistent_megakernel_02_b200 import Kv4Cache
+
+    n, d, kvh, rep, prompt, top = 64, 128, 8, 4, 8192, 131072
+    table = torch.zeros((n, top // 64), dtype=torch.int32, device="cuda")
+    cache = Kv4Cache.empty(1, 1, kvh, d, table)
+    cu = ints([0] + [prompt + i for i in range(n)])
+    batch = cache.batch(cu, ints([top] * n), prompt + n - 1, prompt, top)
+    # partial results: a row of D + 4 floats for every query row, head and split; 16 splits at most are
+    # called for, and what a block of 256 rows is not filled by adds one block per sequence
+    rows = (prompt + n) * rep + 256 * (n + 1)
+    assert cache.workspace_bytes(batch, kvh * rep, R.DTYPES[dtype]) <= 16 * rows * kvh * (d + 4) * 4
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("d,kv_heads,lens,new", [
     (64, 8, [3000, 1500, 70, 2900, 1, 0, 2500] + [2999] * 20, [1500, 1, 3, 1, 1, 0, 700] + [1] * 20),
