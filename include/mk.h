@@ -362,7 +362,8 @@ mk_status mk_matvec_engine_status(void* stream);
  * nor read.  (Where cu does not ascend, append and read may leave out further sequences,
  * each as a whole.)  Sequences may share pages that are only read; calls that overlap on the
  * GPU, and the sequences of one call, must not write the same positions, nor may a call read
- * what another writes meanwhile. */
+ * what another writes meanwhile.  A call that finds a CUDA error pending from an earlier one
+ * refuses (MK_ERR_CUDA) and leaves it in place. */
 #define MK_KV4_PAGE 64
 
 typedef struct {

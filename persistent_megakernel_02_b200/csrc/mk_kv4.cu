@@ -264,7 +264,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-mk_status launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
+cudaLaunchConfig_t rows_launch(dim3 grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kRowWarps);
+  cfg.stream = s;
+  return cfg;
+}
 
 template <bool WRITE>
 mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, const mk_kv4_rows* k,
@@ -288,8 +294,10 @@ mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, 
   const int parts = WRITE || dtype != 2 ? 1 : kReadParts<float>;
   const long long ctas = (slots * c->n_kv_heads * parts + kRowWarps - 1) / kRowWarps;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define MK_KV4_ROWS(D, T) rows_kernel<D, T, WRITE><<<(unsigned)ctas, 32 * kRowWarps, 0, s>>>(*c, layer, *b, rows, (int)slots)
+  if (kv4_error_pending()) return MK_ERR_CUDA;
+  const cudaLaunchConfig_t cfg = rows_launch(dim3((unsigned)ctas), static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+#define MK_KV4_ROWS(D, T) e = cudaLaunchKernelEx(&cfg, rows_kernel<D, T, WRITE>, *c, layer, *b, rows, (int)slots)
   if (c->head_dim == 64) {
     if (dtype == 0) MK_KV4_ROWS(64, __nv_bfloat16);
     else if (dtype == 1) MK_KV4_ROWS(64, __half);
@@ -300,7 +308,7 @@ mk_status run_rows(const mk_kv4_cache* c, int32_t layer, const mk_kv4_batch* b, 
     else MK_KV4_ROWS(128, float);
   }
 #undef MK_KV4_ROWS
-  return launched();
+  return kv4_status(e);
 }
 
 }  // namespace
@@ -343,10 +351,11 @@ mk_status kv4_slot(bool write, const mk_kv4_cache* c, void* kv, const int* slot_
   const int n_tiles = (start + n - 1) / kKv4Tile - start / kKv4Tile + 1;
   const long long ctas = ((long long)n_tiles * c->n_kv_heads + kRowWarps - 1) / kRowWarps;
   if (ctas * kRowWarps > 0x7FFFFFFF || c->n_layers > 65535) return MK_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ctas, c->n_layers);
-#define MK_KV4_SLOT(D, T)                                                                                        \
-  (write ? slot_kernel<D, T, true><<<grid, 32 * kRowWarps, 0, s>>>(*c, rows, table_row, start, n, n_tiles)       \
-         : slot_kernel<D, T, false><<<grid, 32 * kRowWarps, 0, s>>>(*c, rows, table_row, start, n, n_tiles))
+  const cudaLaunchConfig_t cfg = rows_launch(dim3((unsigned)ctas, c->n_layers), s);
+  cudaError_t e;
+#define MK_KV4_SLOT(D, T)                                                                                      \
+  e = write ? cudaLaunchKernelEx(&cfg, slot_kernel<D, T, true>, *c, rows, table_row, start, n, n_tiles)        \
+            : cudaLaunchKernelEx(&cfg, slot_kernel<D, T, false>, *c, rows, table_row, start, n, n_tiles)
   if (c->head_dim == 64) {
     if (fp16) MK_KV4_SLOT(64, __half);
     else MK_KV4_SLOT(64, __nv_bfloat16);
@@ -355,7 +364,7 @@ mk_status kv4_slot(bool write, const mk_kv4_cache* c, void* kv, const int* slot_
     else MK_KV4_SLOT(128, __nv_bfloat16);
   }
 #undef MK_KV4_SLOT
-  return launched();
+  return kv4_status(e);
 }
 
 }  // namespace mk

@@ -38,6 +38,16 @@ struct Kv4AttnSplit : Kv4Attn {
   float* part;             // [CTA of the grid: row tile, then split][rows of a tile][D + 4]
 };
 
+// An error that some earlier call left pending is not these calls' to report or to clear: they
+// refuse and leave it in place.
+inline bool kv4_error_pending() { return cudaPeekAtLastError() != cudaSuccess; }
+// Status of a launch (or of what comes before it); its own error is not left pending.
+inline mk_status kv4_status(cudaError_t e) {
+  if (e == cudaSuccess) return MK_OK;
+  cudaGetLastError();
+  return MK_ERR_CUDA;
+}
+
 // Opt-in to more than 48 KiB of shared memory (and to clusters of more than 8 CTAs), once
 // per kernel and device.
 bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready, bool large_cluster = false);

@@ -809,9 +809,9 @@ struct Plan {
 int sm_count() {
   static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (kv4_status(cudaGetDevice(&dev)) != MK_OK) return 0;
   if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (kv4_status(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != MK_OK) return 0;
   if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
@@ -922,7 +922,7 @@ mk_status launch_join(const AttnArgs& a, const Plan& p, cudaStream_t s) {
   cudaError_t e;
   if constexpr (kPrompt) e = cudaLaunchKernelEx(&cfg, attn_join_prompt<D, T>, a);
   else e = cudaLaunchKernelEx(&cfg, attn_join<D, T, ROWS>, a);
-  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return kv4_status(e);
 }
 
 template <int D, class T, int NT>
@@ -944,11 +944,11 @@ mk_status launch_few(const AttnArgs& a, const Plan& p, cudaStream_t s) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, true>, a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    return kv4_status(cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, true>, a));
   }
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_few<D, T, NT, false>), kSmem, &ready, false)) return MK_ERR_CUDA;
-  if (cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, false>, a) != cudaSuccess) return MK_ERR_CUDA;
-  return p.n_split > 1 ? launch_join<D, T, 8 * NT>(a, p, s) : MK_OK;
+  const mk_status st = kv4_status(cudaLaunchKernelEx(&cfg, attn_few<D, T, NT, false>, a));
+  return st == MK_OK && p.n_split > 1 ? launch_join<D, T, 8 * NT>(a, p, s) : st;
 }
 
 template <int D, class T>
@@ -970,11 +970,11 @@ mk_status check_attention(const mk_kv4_cache* c, int32_t layer, const mk_kv4_bat
 
 bool kv4_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready, bool large_cluster) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (kv4_status(cudaGetDevice(&dev)) != MK_OK) return false;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (ready->load(std::memory_order_relaxed) & bit) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  if (large_cluster && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (kv4_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != MK_OK) return false;
+  if (large_cluster && kv4_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != MK_OK)
     return false;
   ready->fetch_or(bit, std::memory_order_relaxed);
   return true;
@@ -1007,6 +1007,7 @@ extern "C" mk_status mk_kv4_attention(const mk_kv4_cache* cache, int32_t layer, 
   st = kv4_check_rows(q, dtype, batch->n_rows, n_heads, cache->head_dim, false);
   if (st == MK_OK) st = kv4_check_rows(out, dtype, batch->n_rows, n_heads, cache->head_dim, true);
   if (st != MK_OK) return st;
+  if (kv4_error_pending()) return MK_ERR_CUDA;
   const int rep = n_heads / cache->n_kv_heads;
   Plan p;
   st = plan_few(cache, batch, rep, dtype, &p);

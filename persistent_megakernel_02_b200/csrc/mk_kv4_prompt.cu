@@ -749,8 +749,12 @@ static mk_status launch(const Kv4AttnSplit& a, cudaStream_t s) {
   if (!kv4_allow_smem(reinterpret_cast<const void*>(attn_prompt<D, T>), kSmem, &ready)) return MK_ERR_CUDA;
   const long long ctas = (a.n_blocks ? a.n_blocks : (long long)a.n_rt * a.b.n_seqs) * a.c.n_kv_heads * a.n_split;
   if (ctas > 0x7FFFFFFF) return MK_ERR_UNSUPPORTED;
-  attn_prompt<D, T><<<(unsigned)ctas, kPThreads, kSmem, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  return kv4_status(cudaLaunchKernelEx(&cfg, attn_prompt<D, T>, a));
 }
 
 mk_status kv4_prompt(const Kv4AttnSplit& a, int32_t dtype, cudaStream_t s) {

@@ -17,7 +17,8 @@ static mk_status move_slot(bool park, mk_handle h, int32_t slot, int32_t start, 
       (long long)start + n > (long long)MK_KV4_PAGE * max_pages)
     return MK_ERR_INVALID_ARG;
   if (n == 0) return MK_OK;
-  cudaSetDevice(h->dev);
+  if (kv4_error_pending()) return MK_ERR_CUDA;
+  MK_TRY(kv4_status(cudaSetDevice(h->dev)));
   return kv4_slot(park, cache, h->kv, h->page_table + (size_t)slot * D.pages_per_seq, D.n_phys_pages, D.PL, D.kv_fp16,
                   block_table_row, start, n, static_cast<cudaStream_t>(stream));
 }

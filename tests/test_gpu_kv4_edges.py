@@ -1,10 +1,15 @@
 """The 4-bit KV cache on the GPU where a call can go wrong: long runs, far ranges, batches of very
 unequal sequences, streams, errors (needs a B200)."""
 
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
+import synth
+from synth import configs
 from tests import _kv4 as R
 from tests.test_gpu_kv4 import Setup
 
@@ -325,3 +330,77 @@ def test_small_values_under_uneven_weights(v_size, d, dtype, grow):
     s.cache.check()
     for i in (0, 24, 26, 119):
         assert norm_error(s.got(out, i), s.want(q, i)) < NORM[dtype], i
+
+
+# ---- streams and errors --------------------------------------------------------------------
+
+
+def tiny(**kw):
+    from persistent_megakernel_02_b200 import Kv4Cache, Megakernel
+
+    cfg = configs.model_config("tiny", max_batch=2, max_seq=160, **kw)
+    mk = Megakernel(cfg, synth.make_weights(cfg, device="cuda"))
+    table = ints([[4, 1, 3], [2, 0, 0]])
+    return mk, cfg, Kv4Cache.empty(cfg["n_layers"], 5, cfg["n_kv_heads"], cfg["head_dim"], table)
+
+
+PENDING = """
+import sys, torch
+sys.path.insert(0, %r)
+from persistent_megakernel_02_b200 import MkError, greedy_head_noalloc, matvec_engine_status
+from tests.test_gpu_kv4 import Setup
+from tests.test_gpu_kv4_edges import tiny
+sets = [Setup(64, 16, [700, 300], [1, 1]), Setup(64, 16, [700, 300], [300, 200]), Setup(64, 2, [9000], [1])]
+for s in sets:
+    s.fill()
+mk, cfg, cache = tiny()
+head = [torch.zeros((1, 64), device="cuda"), torch.zeros(64, dtype=torch.bfloat16, device="cuda"),
+        torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")]
+greedy_head_noalloc(*head, 1e-5, torch.zeros(1, dtype=torch.int32, device="cuda"))  # (its first call sets things up)
+torch.cuda.synchronize()
+try:  # waiting for a stream that is being captured is an error, which stays with the library's runtime
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        try:
+            matvec_engine_status(torch.cuda.current_stream())
+        except MkError:
+            print("refused")
+except Exception as e:
+    print("capture ended")
+torch.cuda.synchronize()
+def refused(fn, *a):
+    try:
+        fn(*a)
+        return False
+    except MkError as e:
+        return e.status == 4
+before = cache.pool.clone()
+for s in sets:
+    pool = s.cache.pool.clone()
+    q = torch.ones((s.rows, 4 * s.kv_heads, 64), dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.full((s.rows, s.kv_heads, 64), 3.0, device="cuda") for _ in range(2))
+    out = torch.full_like(q, -7.0)
+    need = s.cache.workspace_bytes(s.batch, q.shape[1], q.dtype)  # (asks the device, launches nothing)
+    assert refused(s.cache.append, 0, k, v, s.batch) and refused(s.cache.read, 0, k, v, s.batch)
+    assert refused(s.cache.attend, 0, q, out, s.batch)
+    torch.cuda.synchronize()
+    assert (out == -7).all() and (k == 3).all() and (v == 3).all() and torch.equal(pool, s.cache.pool)
+assert refused(mk.park, 0, 5, cache, 0) and refused(mk.resume, 0, 5, cache, 0)
+torch.cuda.synchronize()
+assert torch.equal(before, cache.pool)
+try:
+    greedy_head_noalloc(*head, 1e-5, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    print("error gone")
+except MkError:
+    print("error kept")
+"""
+
+
+def test_an_earlier_error_is_left_in_place():
+    """An error that another call left pending is not these calls': they refuse, launch nothing and leave
+    it, as the other stand-alone stages do."""
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", PENDING % root], capture_output=True, text=True, timeout=600, cwd=root)
+    assert run.returncode == 0, run.stdout + run.stderr
+    assert run.stdout.split("\n")[:3] == ["refused", "capture ended", "error kept"], run.stdout + run.stderr
