@@ -399,18 +399,31 @@ class Megakernel:
                              "cache's device with a row for the sequence")
         if cache.device.index != self._device:
             raise MkError(1, f"{what}: the cache is not on the handle's device ({self._device})")
+        # By default the handle's steps run on the default stream, the cache's calls on torch's current
+        # one: without a stream the copy comes behind what either has so far and before what follows.
+        home, current = torch.cuda.default_stream(cache.device), torch.cuda.current_stream(cache.device)
+        apart = stream is None and current != home
+        if apart and torch.cuda.is_current_stream_capturing():
+            raise MkError(1, f"{what}: name the stream; the default stream, where the handle's steps run "
+                             "without one, cannot be captured")
+        if apart:
+            home.wait_stream(current)
         _check(fn(self._h, slot, start, n, cache._struct, table.data_ptr() + 4 * int(table.shape[1]) * seq,
                   int(table.shape[1]), _stream_handle(stream)), what)
+        if apart:
+            current.wait_stream(home)
 
     def park(self, slot, n, cache, seq, start=0, block_table=None, stream=None):
         """Quantise positions start .. start + n - 1 of slot ``slot``, every layer, into
         sequence ``seq`` of a :class:`Kv4Cache` (a row of its block table); the slot can then
-        take another sequence.  Asynchronous, ordered like the handle's steps."""
+        take another sequence.  Asynchronous.  On ``stream``; without one, behind the handle's steps
+        of the default stream and the cache's calls on torch's current stream, and before what
+        follows on either (inside a graph capture it has to be given)."""
         self._move_slot(lib().mk_kv4_park, "mk_kv4_park", slot, n, cache, seq, start, block_table, stream)
 
     def resume(self, slot, n, cache, seq, start=0, block_table=None, stream=None):
         """Write the parked positions back into slot ``slot`` (any slot), rounded to the
-        handle's K/V type; decoding continues at position start + n."""
+        handle's K/V type; decoding continues at position start + n.  Streams as for :meth:`park`."""
         self._move_slot(lib().mk_kv4_resume, "mk_kv4_resume", slot, n, cache, seq, start, block_table, stream)
 
     def profile_records(self):

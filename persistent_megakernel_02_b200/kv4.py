@@ -8,6 +8,10 @@ current torch stream of the pool's device), check every tensor's type, shape, la
 first and raise :class:`MkError` before anything is launched.  What only the device
 can see (lengths or page ids out of bounds) is recorded in the cache's status word,
 which :meth:`Kv4Cache.check` reads.
+
+The package's other stages (``matvec_engine``, ``greedy_head_noalloc``, a handle's steps) run on
+the default stream unless they are given one: inside ``torch.cuda.stream(s)`` give them ``s``.
+``Megakernel.park`` and ``resume`` without a stream keep the order of both.
 """
 
 from __future__ import annotations

@@ -344,6 +344,100 @@ def tiny(**kw):
     return mk, cfg, Kv4Cache.empty(cfg["n_layers"], 5, cfg["n_kv_heads"], cfg["head_dim"], table)
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_park_and_resume_keep_the_order_of_the_current_stream(given):
+    """The handle's steps run on the default stream unless told otherwise, the cache's calls on torch's
+    current one: without a stream, park and resume come behind both and before what follows on either."""
+    mk, cfg, cache = tiny()
+    prompts = [synth.prompt_tokens(cfg, i, 130).tolist() for i in range(2)]
+    shape = (130, cfg["n_kv_heads"], cfg["head_dim"])
+    batch = cache.batch(ints([0, 130]), ints([130]), 130, 130, 130)
+    want = []
+    for i in range(2):  # what each prompt parks
+        mk.prefill(0, prompts[i])
+        mk.park(0, 130, cache, 0)
+        kv = [torch.empty(shape, device="cuda") for _ in range(2)]
+        cache.read(0, *kv, batch)
+        torch.cuda.synchronize()
+        want.append(kv)
+    assert not torch.equal(want[0][0], want[1][0])
+    side = torch.cuda.Stream()
+    arg = {"stream": side} if given else {}
+    slow = 200_000_000  # cycles, about 0.1 s
+    # the handle's work is late: what is read on the current stream is the new prompt's all the same
+    mk.prefill(0, prompts[0])
+    mk.sync()
+    cache.pool.zero_()
+    torch.cuda.synchronize()
+    got = [torch.empty(shape, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        if not given:
+            with torch.cuda.stream(torch.cuda.default_stream()):
+                torch.cuda._sleep(slow)
+        mk.park(0, 130, cache, 0, **arg)
+        cache.read(0, *got, batch)
+        cache.check()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    # the cache's work is late: what is resumed is what the current stream writes
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(slow)
+        for layer in range(cfg["n_layers"]):
+            cache.append(layer, *want[1], batch)
+        mk.resume(1, 130, cache, 0, **arg)
+        cache.pool.zero_()  # behind the resume
+        mk.park(1, 130, cache, 0, **arg)
+        cache.read(0, *got, batch)
+    torch.cuda.synchronize()
+    # (what came out of a cache goes back into it within one more rounding to the handle's bf16, so
+    # within one step of the grid; another prompt's values are far from that)
+    for a, b in zip(got, want[1]):
+        _, step, _ = R.quantise(b.double().cpu().numpy())
+        assert (np.abs((a - b).double().cpu().numpy()) <= 1.1 * np.repeat(step, 32, -1) + 2.0**-7 * np.abs(b.cpu().numpy())).all()
+    # a page that is missing is reported by a check on the current stream
+    torch.cuda.synchronize()
+    cache.block_table[0, 1] = 99
+    torch.cuda.synchronize()
+    from persistent_megakernel_02_b200 import MkError
+
+    with torch.cuda.stream(side):
+        if not given:
+            with torch.cuda.stream(torch.cuda.default_stream()):
+                torch.cuda._sleep(slow)
+        mk.park(0, 130, cache, 0, **arg)
+        with pytest.raises(MkError, match="a page id"):
+            cache.check()
+    torch.cuda.synchronize()
+    mk.close()
+
+
+def test_park_without_a_stream_inside_a_capture_is_refused():
+    """The default stream cannot be captured; with the capturing stream the copy is captured and replays."""
+    from persistent_megakernel_02_b200 import MkError
+
+    mk, cfg, cache = tiny()
+    mk.prefill(0, synth.prompt_tokens(cfg, 1, 100).tolist())
+    mk.park(0, 100, cache, 0)
+    mk.sync()
+    want = cache.pool.clone()
+    cache.pool.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(MkError, match="INVALID_ARG"):
+            mk.park(0, 100, cache, 0)
+        mk.park(0, 100, cache, 0, stream=torch.cuda.current_stream())
+    cache.pool.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    pages = cache.block_table[0, :2].long()
+    assert torch.equal(cache.pool[:, pages[0]], want[:, pages[0]])
+    graph.reset()
+    mk.close()
+
+
 PENDING = """
 import sys, torch
 sys.path.insert(0, %r)
