@@ -391,6 +391,10 @@ typedef struct {
   int64_t row_stride, head_stride;
 } mk_kv4_rows;
 
+/* Take the status word's bits: *bits (device) becomes the word and the word zero, in one step,
+ * so that nothing is lost which a call on another stream reports meanwhile.  Asynchronous. */
+mk_status mk_kv4_take_status(const mk_kv4_cache* cache, uint32_t* bits, void* stream);
+
 /* Bytes of one page of one kv head; 0 for an unsupported head_dim. */
 int64_t mk_kv4_page_bytes(int32_t head_dim);
 

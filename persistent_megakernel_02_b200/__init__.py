@@ -145,6 +145,7 @@ _SIGS = {
                                         ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                         ctypes.c_int32, ctypes.c_void_p]),
     "mk_matvec_engine_status": (ctypes.c_int, [ctypes.c_void_p]),
+    "mk_kv4_take_status": (ctypes.c_int, [ctypes.POINTER(MkKv4CacheStruct), ctypes.c_void_p, ctypes.c_void_p]),
     "mk_kv4_page_bytes": (ctypes.c_int64, [ctypes.c_int32]),
     "mk_kv4_append": (ctypes.c_int, _KV4_ROWS + [ctypes.c_int32, ctypes.c_void_p]),
     "mk_kv4_read": (ctypes.c_int, _KV4_ROWS + [ctypes.c_int32, ctypes.c_void_p]),

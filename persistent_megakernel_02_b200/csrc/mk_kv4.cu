@@ -262,6 +262,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
   do_tile<D, T, WRITE>(c, j, rows, head, 0);
 }
 
+__global__ void take_status_kernel(uint32_t* status, uint32_t* bits) { *bits = atomicExch(status, 0u); }
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 cudaLaunchConfig_t rows_launch(dim3 grid, cudaStream_t s) {
@@ -373,6 +375,17 @@ using namespace mk;
 
 extern "C" int64_t mk_kv4_page_bytes(int32_t head_dim) {
   return head_dim == 64 || head_dim == 128 ? (int64_t)kKv4Tiles * 20 * head_dim : 0;
+}
+
+extern "C" mk_status mk_kv4_take_status(const mk_kv4_cache* cache, uint32_t* bits, void* stream) {
+  const mk_status st = kv4_check_cache(cache);
+  if (st != MK_OK) return st;
+  if (!bits || ((uintptr_t)bits & 3u)) return MK_ERR_INVALID_ARG;
+  if (kv4_error_pending()) return MK_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = cfg.blockDim = dim3(1);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  return kv4_status(cudaLaunchKernelEx(&cfg, take_status_kernel, cache->status, bits));
 }
 
 extern "C" mk_status mk_kv4_append(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_batch* batch,

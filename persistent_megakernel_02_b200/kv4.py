@@ -198,11 +198,13 @@ class Kv4Cache:
 
     def check(self, stream=None):
         """Wait for ``stream`` and raise MkError if a call met numbers outside its batch's
-        bounds or a page id outside the pool since the last check."""
+        bounds or a page id outside the pool since the last check.  One that another stream's call
+        meets meanwhile is reported by this check or the next one."""
         raw = self._launch("Kv4Cache.check", stream)
         with torch.cuda.stream(self._torch_stream(raw)):
-            bits = int(self._status.item())
-            self._status.zero_()
+            taken = torch.empty(1, dtype=torch.int32, device=self.device)
+            _check(lib().mk_kv4_take_status(self._struct, taken.data_ptr(), raw), "mk_kv4_take_status")
+            bits = int(taken.item())
         if bits & 4:
             raise MkError(5, "Kv4Cache: a bounded wait ran out")
         if bits:

@@ -438,6 +438,34 @@ def test_park_without_a_stream_inside_a_capture_is_refused():
     mk.close()
 
 
+def test_no_report_is_lost_between_two_streams():
+    """A call on one stream meets a bad page while a check runs on another: that check or the next
+    one says so."""
+    from persistent_megakernel_02_b200 import MkError
+
+    s = Setup(64, 2, [40], [40])
+    s.fill()
+    q = s.rand(40, 8, "bf16")
+    out = torch.empty_like(q)
+    s.table[0, 0] = s.cache.n_pages
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def reported(stream):
+        try:
+            s.cache.check(stream=stream)
+        except MkError:
+            return True
+        return False
+
+    for i in range(1500):
+        with torch.cuda.stream(one):
+            torch.cuda._sleep(1000 + 97 * (i % 700))  # 1 to 36 us
+        s.cache.attend(0, q, out, s.batch, stream=one)
+        early = reported(two)
+        assert reported(one) or early, i
+
+
 PENDING = """
 import sys, torch
 sys.path.insert(0, %r)
