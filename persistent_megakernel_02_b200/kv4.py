@@ -89,6 +89,9 @@ class Kv4Cache:
         self.device = pool.device
         self.n_layers, self.n_pages, self.n_kv_heads = (int(x) for x in pool.shape[:3])
         self._status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        with torch.cuda.device(pool.device):
+            if not torch.cuda.is_current_stream_capturing():  # calls on any stream come behind the zero
+                torch.cuda.current_stream().synchronize()
         self._struct = MkKv4CacheStruct(pool.data_ptr(), self._status.data_ptr(), self.n_layers, self.n_pages,
                                         self.n_kv_heads, self.head_dim)
         self._index = pool.device.index

@@ -466,6 +466,25 @@ def test_no_report_is_lost_between_two_streams():
         assert reported(one) or early, i
 
 
+def test_a_new_cache_may_be_used_on_any_stream_at_once():
+    """Its status word is cleared before the constructor returns, also where its stream is busy."""
+    from persistent_megakernel_02_b200 import Kv4Cache, MkError
+
+    s = Setup(64, 2, [40], [40])
+    q = s.rand(40, 8, "bf16")
+    out = torch.empty_like(q)
+    s.table[0, 0] = s.cache.n_pages
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    cache = Kv4Cache(s.cache.pool, s.table, 64)
+    cache.attend(0, q, out, s.batch, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    with pytest.raises(MkError, match="a page id"):
+        cache.check(stream=side)
+
+
 PENDING = """
 import sys, torch
 sys.path.insert(0, %r)
