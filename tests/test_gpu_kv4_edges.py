@@ -133,6 +133,37 @@ def test_a_few_rows_of_many_long_sequences(d, new, dtype):
         assert norm_error(s.got(out, i), s.want(q, i)) < NORM[dtype]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 1), (64, 4), (128, 4), (64, 40), (128, 40)])
+def test_missing_pages_of_many_long_sequences(d, new, dtype):
+    """Each page has values of its own and weights are nearly even, so a page that is left in or out
+    wrongly moves the result by several per cent; pages far into a warp's run among them."""
+    from persistent_megakernel_02_b200 import MkError
+
+    n_len, gone = 9000, (0, 3, 31, 66, 67, 100, 131)
+    pages = torch.randn((-(-n_len // 64), 8, d), generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    spread = pages.repeat_interleave(64, 0)[:n_len]
+    s = Shared(d, 8, n_len, [n_len - 7 * (i % 9) for i in range(90)], new=[new] * 90, make_k=lambda k: k * 0.1,
+               make_v=lambda v: 0.2 * v + spread)
+    q = s.queries(16, dtype)
+    whole = s.want(q, 4)
+    for i, page in enumerate(gone):
+        s.table[:, page] = (-1, s.cache.n_pages, -2, 2**31 - 1)[i % 4]
+    out = s.attend(q)
+    with pytest.raises(MkError, match="a page id"):
+        s.cache.check()
+    keep = torch.ones(n_len, dtype=torch.bool, device="cuda")
+    for page in gone:
+        keep[64 * page:64 * page + 64] = False
+    t = Shared.__new__(Shared)
+    t.__dict__.update(s.__dict__)
+    t.k, t.v, t.lens = s.k[keep], s.v[keep], [n - 64 * len(gone) for n in s.lens]
+    for i in (0, 4, 89):
+        # (of prompts K and V are rounded as well, one more of 2.1e-4 each)
+        assert norm_error(s.got(out, i), t.want(q, i)) < (NORM[dtype] if new < 40 or dtype == "fp32" else NORM[dtype] + 2.4e-4)
+    assert norm_error(s.got(out, 4), whole) > 0.03
+
+
 # ---- a whole batch's bounds and a sequence's own ------------------------------------------
 
 
