@@ -11,7 +11,7 @@ import torch
 import synth
 from synth import configs
 from tests import _kv4 as R
-from tests.test_gpu_kv4 import Setup
+from tests.test_gpu_kv4 import Setup, check_attention, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -520,7 +520,7 @@ PENDING = """
 import sys, torch
 sys.path.insert(0, %r)
 from persistent_megakernel_02_b200 import MkError, greedy_head_noalloc, matvec_engine_status
-from tests.test_gpu_kv4 import Setup
+from tests.test_gpu_kv4 import Setup, check_attention, reference
 from tests.test_gpu_kv4_edges import tiny
 sets = [Setup(64, 16, [700, 300], [1, 1]), Setup(64, 16, [700, 300], [300, 200]), Setup(64, 2, [9000], [1])]
 for s in sets:
@@ -576,3 +576,65 @@ def test_an_earlier_error_is_left_in_place():
     run = subprocess.run([sys.executable, "-c", PENDING % root], capture_output=True, text=True, timeout=600, cwd=root)
     assert run.returncode == 0, run.stdout + run.stderr
     assert run.stdout.split("\n")[:3] == ["refused", "capture ended", "error kept"], run.stdout + run.stderr
+
+
+# ---- inputs and bounds -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("new", [1, 3, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite_reach_only_their_rows(bad, new, dtype):
+    s = Setup(64, 16, [700, 500, 400], [new] * 3)
+    s.fill()
+    q = s.rand(s.rows, 64, dtype)
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    s.cache.attend(0, q, clean, s.batch)
+    hit = torch.zeros((s.rows, 64), dtype=torch.bool, device="cuda")
+    for row, head, value in ((0, 0, 7), (s.rows - 1, 5, 0), (s.rows // 2, 63, 63)):
+        q[row, head, value] = bad
+        hit[row, head] = True
+    s.cache.attend(0, q, out, s.batch)
+    s.cache.check()
+    assert not torch.isfinite(out[hit]).any()
+    assert torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,new,kv_heads", [([1500, 900], [1, 1], 8), ([9000], [1], 2), ([300] * 40 + [700], [1] * 40 + [300], 8),
+                                               ([600, 500], [257, 64], 16), ([64], [64], 1)])
+def test_bounds_wider_than_the_batch(lens, new, kv_heads, dtype):
+    """As a captured step has them: room for more rows, longer spans and lengths than there are."""
+    s = Setup(64, kv_heads, lens, new)
+    kv = s.fill()
+    pad = 900
+    table = torch.full((len(lens), 2048), -1, dtype=torch.int32, device="cuda")
+    table[:, :s.table.shape[1]] = s.table
+    q = s.rand(s.rows + pad, 4 * kv_heads, dtype)
+    k, v = (torch.full((s.rows + pad, kv_heads, 64), -7.0, dtype=q.dtype, device="cuda") for _ in range(2))
+    for max_new, max_len in ((max(new), 131072), (s.rows + pad, 20000), (s.rows + pad, 131072)):
+        batch = s.cache.batch(s.cu, s.kv_lens, s.rows + pad, max_new, max_len, block_table=table)
+        out = torch.full_like(q, -7.0)
+        s.cache.attend(0, q, out, batch)
+        s.cache.read(0, k, v, batch)
+        s.cache.check()
+        for i, (n_len, n) in enumerate(zip(lens, new)):
+            a, b = s.cu_np[i], s.cu_np[i + 1]
+            want, _ = reference(s, kv, q, i, R.default_scale(64))
+            want = torch.from_numpy(want).cuda()
+            assert norm_error(out[a:b].double(), want) < (NORM[dtype] if dtype == "fp32" else NORM[dtype] + 2.4e-4)
+            for t, x in ((k, kv[i][0]), (v, kv[i][1])):
+                assert torch.equal(t[a:b].cpu(), torch.from_numpy(x[n_len - n:]).float().to(q.dtype))
+        for t in (out, k, v):
+            assert (t[s.rows:] == -7.0).all()
+
+
+@pytest.mark.parametrize("new", [1, 300])
+def test_broadcast_queries(new):
+    """One query for all heads, or for all rows: strides of zero."""
+    s = Setup(128, 16, [500, 400], [new, new])
+    kv = s.fill()
+    for q in (s.rand(s.rows, 1, "bf16").expand(s.rows, 32, 128), s.rand(1, 32, "bf16").expand(s.rows, 32, 128)):
+        out = torch.empty((s.rows, 32, 128), dtype=torch.bfloat16, device="cuda")
+        s.cache.attend(0, q, out, s.batch)
+        check_attention(s, kv, q, out, "bf16")
