@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 ? 5 : 7)
   const int head = (int)(g % c.n_kv_heads), part = (int)(g / c.n_kv_heads % kParts);
   const int slot = (int)(g / (c.n_kv_heads * kParts));
   if (slot >= n_slots) return;
-  if ((threadIdx.x & 31) == 0) kv4_report_order(c, b, g);  // (two slots or more to a sequence)
   const TileJob j = tile_job(c, b, layer, slot);
   if (j.ok) do_tile<D, T, WRITE>(c, j, rows, head, part);
+  if ((threadIdx.x & 31) == 0) kv4_report_order(c, b, g);  // (two slots or more to a sequence)
 }
 
 // Positions start .. start + n - 1 of a handle's slot: warps over (tile, kv head), grid.y
