@@ -92,7 +92,7 @@ __device__ __forceinline__ uint32_t high_v(uint32_t x) {
   x &= 0x00F000F0u;
   return CENTRE ? hfma2(x, 0x68006800u, 0xA380A380u) : x;
 }
-// Sums over more than 16 positions are kept out of the matrix unit: it cuts its sums off
+// Sums over more than 32 positions are kept out of the matrix unit: it cuts its sums off
 // instead of rounding them, the codes' sums all grow in one direction, and the minima's part
 // largely takes them back (fp16, 150 sequences of 16384 positions with even weights: results
 // 4.5e-3 off in the 2-norm with the sums kept there, of 131072 4.4e-2).
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
   // are 5.1e-4 off instead of their own rounding's 2.1e-4; bf16's is 1.7e-3.)
   constexpr bool kExact = kF32 || std::is_same<T, __half>::value;
   // Values as (z + 7.5 s) + s (c - 7.5): neither part has a mean of its own, so that long sums do
-  // not grow only to cancel (2048 of a tile's products added in 32 bits, 131072 positions: 4e-4 off
+  // not grow only to cancel (1024 sums of 32 positions added in 32 bits, 131072 positions: 4e-4 off
   // in the 2-norm without).  It costs little where codes are made normal numbers anyway: the sum
   // over a tile of w s is in rows 8..15 of the minima's product, which would be idle.  16-bit calls
   // bound the sum's length instead (all types so: 64 long sequences 153 -> 170 us).
@@ -489,16 +489,13 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
             for (int i = 0; i < 4; ++i) o[t][g][j][i] *= ((i & 1) ? c1 : c0) * less;
       }
     }
-    // weights and values
+    // weights, and the minima's product
+    uint32_t vs[SUB][2 * G], wp[SUB][NT][2];  // weights of positions 2 tig, 2 tig + 1 (+ 8)
+    [[maybe_unused]] float w[SUB][NT][4];
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
       const uint8_t* tile = tiles + u * L::kBytes;
-      uint32_t vs[2 * G], vz[2], sz[2];  // sz: scales of group gid, as rows 8..15 of the minima's operand
-#pragma unroll
-      for (int v = 0; v < 2 * G / 4; ++v) {
-        const uint4 y = lds_u4(tile + L::kVs + v * 64 + tig * 16);
-        vs[4 * v] = y.x; vs[4 * v + 1] = y.y; vs[4 * v + 2] = y.z; vs[4 * v + 3] = y.w;
-      }
+      uint32_t vz[2], sz[2];  // sz: scales of group gid, as rows 8..15 of the minima's operand
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         vz[n] = gid < G ? lds_u1(tile + L::kVz + gid * 32 + n * 16 + tig * 4) : gid == G ? 0x3C003C00u : 0u;
@@ -510,72 +507,95 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
           sz[n] = finite2(sz[n]) & keep;
         }
       }
-      uint32_t wp[NT][2], wl[NT][2];  // weights of positions 2 tig, 2 tig + 1 (+ 8); low parts
-      float w[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        float x[4];
+        uint32_t wl[2];  // low parts
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           // (the difference first: scores far from zero keep their order, and equal ones their weights)
           const float2 e = __ffma2_rn(__fadd2_rn(make_float2(s[t][u][i], s[t][u][i + 1]), make_float2(-peak[t], -peak[t])),
                                       make_float2(kscale[t], kscale[t]), make_float2((float)lift, (float)lift));
-          w[t][i] = ex2(e.x);
-          w[t][i + 1] = ex2(e.y);
+          x[i] = ex2(e.x);
+          x[i + 1] = ex2(e.y);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          if constexpr (kF32) split2(w[t][2 * n], w[t][2 * n + 1], wp[t][n], wl[t][n]);
-          else wp[t][n] = pack_h(w[t][2 * n], w[t][2 * n + 1]);
+          if constexpr (kF32) split2(x[2 * n], x[2 * n + 1], wp[u][t][n], wl[n]);
+          else wp[u][t][n] = pack_h(x[2 * n], x[2 * n + 1]);
         }
+        if constexpr (kF32) w[u][t][0] = x[0], w[u][t][1] = x[1], w[u][t][2] = x[2], w[u][t][3] = x[3];
         float z[4];
         if constexpr (kF32) {
-          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wl[t][0], wl[t][1]);
-          mma16816(z, vz[0], sz[0], vz[1], sz[1], wp[t][0], wp[t][1]);
+          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wl[0], wl[1]);
+          mma16816(z, vz[0], sz[0], vz[1], sz[1], wp[u][t][0], wp[u][t][1]);
         } else {
-          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wp[t][0], wp[t][1]);
+          mma16816_zero(z, vz[0], sz[0], vz[1], sz[1], wp[u][t][0], wp[u][t][1]);
         }
         oz[t][0] += kCentre ? fmaf(middle, z[2], z[0]) : z[0];
         oz[t][1] += kCentre ? fmaf(middle, z[3], z[1]) : z[1];
       }
-      uint32_t vc[2 * G];
+    }
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int v = 0; v < 2 * G / 4; ++v) {
-        const uint4 x = lds_u4(tile + L::kV + v * 512 + lane * 16);
-        vc[4 * v] = x.x; vc[4 * v + 1] = x.y; vc[4 * v + 2] = x.z; vc[4 * v + 3] = x.w;
+        const uint4 y = lds_u4(tiles + u * L::kBytes + L::kVs + v * 64 + tig * 16);
+        vs[u][4 * v] = y.x; vs[u][4 * v + 1] = y.y; vs[u][4 * v + 2] = y.z; vs[u][4 * v + 3] = y.w;
       }
+    // values, a group of both tiles at a time
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint32_t x0 = vc[2 * g], x1 = vc[2 * g + 1], y0 = x0 >> 8, y1 = x1 >> 8;
-        const uint32_t a0 = low_v<kCentre>(x0), a1 = high_v<kCentre>(x0), a2 = low_v<kCentre>(x1), a3 = high_v<kCentre>(x1);
-        const uint32_t b0 = low_v<kCentre>(y0), b1 = high_v<kCentre>(y0), b2 = low_v<kCentre>(y1), b3 = high_v<kCentre>(y1);
+    for (int g2 = 0; g2 < G; g2 += 2) {
+      uint4 vc[SUB];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          uint32_t p[2], q[2];
+      for (int u = 0; u < SUB; ++u) vc[u] = lds_u4(tiles + u * L::kBytes + L::kV + g2 / 2 * 512 + lane * 16);
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t sc = vs[n * G + g];
-            if constexpr (kF32) split2(w[t][2 * n] * h_lo(sc), w[t][2 * n + 1] * h_hi(sc), p[n], q[n]);
-            else if constexpr (kExact) split2(h_lo(wp[t][n]) * h_lo(sc), h_hi(wp[t][n]) * h_hi(sc), p[n], q[n]);
-            else p[n] = hmul2(wp[t][n], sc);
-            if constexpr (kMasked) {  // a scale behind the mask may be anything
-              const int at = pos + 16 * u + 8 * n + 2 * tig;
-              const uint32_t keep = (at < lim[t] && at < p1 ? 0xFFFFu : 0u) | (at + 1 < lim[t] && at + 1 < p1 ? 0xFFFF0000u : 0u);
-              p[n] &= keep;
-              if constexpr (kExact) q[n] &= keep;
+      for (int g = g2; g < g2 + 2; ++g) {
+        float y0[NT][4], y1[NT][4];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const uint32_t x0 = g & 1 ? vc[u].z : vc[u].x, x1 = g & 1 ? vc[u].w : vc[u].y, x2 = x0 >> 8, x3 = x1 >> 8;
+          const uint32_t a0 = low_v<kCentre>(x0), a1 = high_v<kCentre>(x0), a2 = low_v<kCentre>(x1), a3 = high_v<kCentre>(x1);
+          const uint32_t b0 = low_v<kCentre>(x2), b1 = high_v<kCentre>(x2), b2 = low_v<kCentre>(x3), b3 = high_v<kCentre>(x3);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint32_t p[2], q[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t sc = vs[u][n * G + g];
+              if constexpr (kF32) split2(w[u][t][2 * n] * h_lo(sc), w[u][t][2 * n + 1] * h_hi(sc), p[n], q[n]);
+              else if constexpr (kExact) split2(h_lo(wp[u][t][n]) * h_lo(sc), h_hi(wp[u][t][n]) * h_hi(sc), p[n], q[n]);
+              else p[n] = hmul2(wp[u][t][n], sc);
+              if constexpr (kMasked) {  // a scale behind the mask may be anything
+                const int at = pos + 16 * u + 8 * n + 2 * tig;
+                const uint32_t keep = (at < lim[t] && at < p1 ? 0xFFFFu : 0u) | (at + 1 < lim[t] && at + 1 < p1 ? 0xFFFF0000u : 0u);
+                p[n] &= keep;
+                if constexpr (kExact) q[n] &= keep;
+              }
+            }
+            if constexpr (kExact) {
+              if (u == 0) {
+                mma16816_zero(y0[t], a0, a1, a2, a3, q[0], q[1]);
+                mma16816_zero(y1[t], b0, b1, b2, b3, q[0], q[1]);
+              } else {
+                mma16816(y0[t], a0, a1, a2, a3, q[0], q[1]);
+                mma16816(y1[t], b0, b1, b2, b3, q[0], q[1]);
+              }
+              mma16816(y0[t], a0, a1, a2, a3, p[0], p[1]);
+              mma16816(y1[t], b0, b1, b2, b3, p[0], p[1]);
+            } else if (u == 0) {
+              mma16816_zero(y0[t], a0, a1, a2, a3, p[0], p[1]);
+              mma16816_zero(y1[t], b0, b1, b2, b3, p[0], p[1]);
+            } else {
+              mma16816(y0[t], a0, a1, a2, a3, p[0], p[1]);
+              mma16816(y1[t], b0, b1, b2, b3, p[0], p[1]);
             }
           }
-          float y0[4], y1[4];
-          if constexpr (kExact) {
-            mma16816_zero(y0, a0, a1, a2, a3, q[0], q[1]);
-            mma16816_zero(y1, b0, b1, b2, b3, q[0], q[1]);
-            mma16816(y0, a0, a1, a2, a3, p[0], p[1]);
-            mma16816(y1, b0, b1, b2, b3, p[0], p[1]);
-          } else {
-            mma16816_zero(y0, a0, a1, a2, a3, p[0], p[1]);
-            mma16816_zero(y1, b0, b1, b2, b3, p[0], p[1]);
-          }
-          add4(o[t][g][0], y0);
-          add4(o[t][g][1], y1);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          add4(o[t][g][0], y0[t]);
+          add4(o[t][g][1], y1[t]);
         }
       }
     }
