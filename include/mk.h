@@ -412,7 +412,14 @@ mk_status mk_kv4_read(const mk_kv4_cache* cache, int32_t layer, const mk_kv4_bat
  *   out[r][h] = sum_p softmax_p(scale * q[r][h] . K[p][h / rep]) V[p][h / rep],
  * p over positions 0 .. kv_lens[i] - (cu[i+1] - cu[i]) + j of row j of sequence i,
  * rep = n_heads / n_kv_heads in {1, 2, 4, 8}.  A row that sees no position (its
- * sequence is shorter than its span) is zero.  Scores, softmax and sums are fp32.
+ * sequence is shorter than its span) is zero.  Scores, the softmax's maximum and sum and
+ * the sums over positions are fp32.  Weights are fp16: two parts of 22 bits together for
+ * fp32 queries, one for 16-bit ones, for bf16 rounded once more with V's scale.  Over many
+ * rows of 16-bit queries K and V are fp16, K (and V of 64-value heads) in two parts for fp16
+ * queries, in one for bf16.  Off in the 2-norm, up to 131072 positions: fp32 2e-6, fp16
+ * 3e-4 (many rows of 128-value heads 3.6e-4), bf16 1.7e-3 to 1.9e-3, their own rounding being
+ * 2.1e-4 and 1.7e-3; many rows of bf16 queries over keys that all have a channel 100 from
+ * zero 2.4e-3, 300 8.9e-3 (fp16 queries keep 3e-4).
  * One new token per sequence or a few, whole prompts, and any mix run here; work is
  * split along the positions when there are few rows or very many positions, which
  * takes `workspace` (device, 16-byte aligned, mk_kv4_attention_workspace bytes, NULL when

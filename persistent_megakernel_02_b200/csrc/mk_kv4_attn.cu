@@ -16,8 +16,8 @@
 // Bytes bound it for long contexts: 20 D bytes per 16 positions and kv head, read once.
 // A warp takes whole stages of 5120 bytes (4 tiles of 64-value heads, 2 of 128) through
 // a ring of bulk copies of its own, so no barrier is met until the warps' states are
-// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 150 us, 4.7 TB/s,
-// 0.71 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 59 us for 32
+// merged.  64 sequences of 823 to 16384 positions x 8 kv heads x 128: 149 us, 4.7 TB/s,
+// 0.71 of the copy rate; the copies alone take 117 (64-value heads: 24 sequences 58 us for 32
 // of bytes).  Fewer registers for a fifth CTA on the SM spill and lose (267 us).  Splits along
 // the positions, where rows are few, are joined in the cluster's shared memory or by a second
 // small kernel.
@@ -39,7 +39,7 @@ constexpr int kWarps = 4;
 constexpr int kThreadsA = 32 * kWarps;
 constexpr int kStageBytes = 5120;
 constexpr int kStages = 2;  // ring depth per warp
-constexpr int kHead = 4;    // log2 of what a weight may pass the reference by
+constexpr int kHead = 4;    // log2 of what a weight may pass the peak's by
 
 using AttnArgs = Kv4AttnSplit;
 
@@ -899,7 +899,7 @@ mk_status plan_few(const mk_kv4_cache* c, const mk_kv4_batch* b, int rep, int dt
   // (one sequence of 8200 positions, 8 kv heads of 64: 15.9 us with 4 splits, 9.1 with 32);
   // and where there are more, up to eight CTAs per SM in pieces of 32 pages, so that
   // sequences of unequal length fill the SMs evenly (64 of up to 16384 positions, kv heads
-  // of 128: 190 us unsplit, 150 so; 64 of about 2000 lose by a split, 55 to 65 us).
+  // of 128: 190 us unsplit, 149 so; 64 of about 2000 lose by a split, 55 to 65 us).
   // A sum of 32 bits that a warp keeps over more than 4096 positions shows in 16-bit results, whose
   // codes' and minima's parts cancel: at most 16384 to a split in any case.
   const long long least = dtype == 2 ? 1 : std::max(1ll, (pages + 255) / 256);

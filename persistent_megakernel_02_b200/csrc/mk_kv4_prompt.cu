@@ -12,21 +12,24 @@
 // half's scores are under way meanwhile, K's buffers are freed apart from V's, and each
 // query tile has an issuing warp of its own, so that neither waits for the other.
 //
-// For bf16 calls K and V are z + s c rounded once to fp16 (2^-11, an eighth of the output's
-// own rounding).  For fp16 calls that would show, K's most of all, as it grows with the scores:
+// For bf16 calls K and V are z + s c rounded once to fp16.  V's rounding, 2^-11, is an eighth of
+// the output's own.  K's moves a score by up to 2^-11 of its largest products, so it grows with
+// the keys: in the 2-norm 1.7e-3 off, as single tokens are, where no channel of all keys is more
+// than 30 from zero, 2.4e-3 at 100, 8.9e-3 at 300 (two parts as below: 1.7e-3 throughout, but
+// 2048 tokens of 128-value heads take 70 us instead of 58).  For fp16 calls both would show:
 // there K, and V of 64-value heads, are two fp16 parts, good to 2^-17 together, and take two
-// products.  Errors in the 2-norm, 2048 tokens over 8192 positions: 7.2e-4 rounded, 2.7e-4 so,
-// the output's own rounding 2.1e-4; 217 us became 254, with 128-value heads 292 became 366
-// (V in two parts too: 572).  Queries are scaled by a power of two per row, which is exact in
-// fp16 but for values 2^-24 below the row's largest, weights are rounded to fp16.  The order
-// of values inside 8 and of positions inside 32 is the one the codes come in: queries are
-// permuted alike, and S, W and V share the order of positions.  O is rescaled only when a
-// score passes the row's reference by more than 16x.
+// products.  Errors in the 2-norm, 2048 tokens over 8192 positions: 7.2e-4 rounded, 2.8e-4 so,
+// the output's own rounding 2.1e-4; 260 us for bf16's 223, with 128-value heads 376 for 296 (V
+// in two parts too: 572).  Queries are scaled by a power of two per row, which is exact in fp16
+// but for values 2^-24 below the row's largest, weights are rounded to fp16.  The order of
+// values inside 8 and of positions inside 32 is the one the codes come in: queries are permuted
+// alike, and S, W and V share the order of positions.  O is rescaled only when a score passes
+// the row's peak by more than 16x.
 //
 // Bound: with 64-value heads the exponentials, 16 per SM and cycle: 2048 cycles for the
 // 256 x 128 scores of a tile, 1024 for its products.  A tile takes about 3500 (1.85 us), the
-// warps' instructions in between: 2048 bf16 tokens x 32 heads over 8192 positions 216 us, 550
-// TFLOP/s; 2048 tokens of 128-value heads, causal, 55 us, 620 TFLOP/s.  (Three or four
+// warps' instructions in between: 2048 bf16 tokens x 32 heads over 8192 positions 223 us, 540
+// TFLOP/s; 2048 tokens of 128-value heads, causal, 58 us, 590 TFLOP/s.  (Three or four
 // query tiles, which would fill the exponential unit, do not fit tensor memory; sixteen
 // softmax warps for the two, 32 columns each, measured 267 us for the former.)
 #include <cuda_runtime.h>
@@ -43,8 +46,8 @@ namespace {
 
 constexpr int kPThreads = 14 * 32;
 constexpr int kPTile = 128;  // positions per tile, and rows per query tile
-constexpr int kPHead = 4;    // log2 of what a weight may pass the reference by
-constexpr int kPLift = 10;   // weights are 2^(score - m + kPLift), at most 2^14
+constexpr int kPHead = 4;    // log2 of what a weight may pass the peak's by
+constexpr int kPLift = 10;   // log2 of the peak's weight: none is above 2^14
 
 // K and V buffers: two of a tile; where K's or V's values have two parts they are of a half
 // tile, and four of them with 64-value heads.  (With 128-value heads there is room for two

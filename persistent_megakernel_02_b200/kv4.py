@@ -161,7 +161,8 @@ class Kv4Cache:
 
     def attend(self, layer, q, out, batch, scale=None, workspace=None, stream=None):
         """Causal attention of query rows ``q`` [n_rows, n_heads, head_dim] over the cache,
-        each row seeing the positions up to its own; ``out`` like ``q``, or ``q`` itself.  ``scale`` defaults to
+        each row seeing the positions up to its own; ``out`` like ``q``, or ``q`` itself.  Many bf16 rows lose
+        accuracy over keys with channels beyond 100, fp16 ones do not (figures in mk.h).  ``scale`` defaults to
         1 / sqrt(head_dim).  ``workspace``: a uint8 CUDA tensor of ``workspace_bytes`` for calls
         that must not allocate; otherwise one is allocated on the launch stream."""
         what = "mk_kv4_attention"
