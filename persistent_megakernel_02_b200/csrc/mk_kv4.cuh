@@ -156,6 +156,27 @@ __device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, uint32_
   return false;
 }
 
+// ---- arithmetic of the attention kernels ----
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // at the rate of a maximum of two
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // What accumulated scores are multiplied by to be in powers of two, kept finite: where it is not
 // (queries beyond 2^100, a scale beyond 1e34) scores that differ at all do so by 2^-72 of the
 // accumulated ones, so that the largest has all the weight with 2^127 too.  Never zero: it

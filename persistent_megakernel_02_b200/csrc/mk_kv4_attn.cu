@@ -57,15 +57,6 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t k) {
-  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                            *reinterpret_cast<const __half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // Two codes of a word as operands, c and c' of one half each: their bits as they are, the
 // subnormals c 2^-24 (16 c 2^-24 from the second nibbles), or NORMAL numbers c (16 c).  The
 // matrix unit aligns products by the exponents of their operands, and a subnormal's is the
@@ -103,16 +94,6 @@ __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
 }
 __device__ __forceinline__ uint4 lds_u4(const uint8_t* p) { return lds128(smem_u32(p)); }
 __device__ __forceinline__ uint32_t lds_u1(const uint8_t* p) { return lds32(smem_u32(p)); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {  // at the rate of a maximum of two
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);

@@ -147,26 +147,6 @@ __device__ __forceinline__ void tmem_get64(uint32_t taddr, uint32_t (&r)[64]) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float pex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {  // at the rate of a maximum of two
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                            *reinterpret_cast<const __half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // The 8 values of a code word as four pairs (nibbles 0 and 4, 1 and 5, 2 and 6, 3 and 7),
 // each z + s c rounded once: a code or'ed into the mantissa of 1024 and taken back out.
 __device__ __forceinline__ void dequant8(uint32_t x, uint32_t s2, uint32_t z2, uint32_t (&v)[4]) {
@@ -388,7 +368,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       if (__any_sync(0xFFFFFFFFu, mx > bound)) {  // the peak moves: seldom
         const bool first = bound == -INFINITY;  // nothing kept so far (but a NaN, which stays one)
         const float now = first ? mx : fmaxf(peak, mx), b = now == -INFINITY ? 0.f : now;
-        const float corr = first ? 0.f : pex2((peak - b) * kscale);
+        const float corr = first ? 0.f : ex2((peak - b) * kscale);
         peak = b;
         bound = __fadd_rd(now, kPHead / kscale);  // (never more than kPHead above)
         sum *= corr;
@@ -415,8 +395,8 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
         for (int c = 0; c < 32; c += 2) {
           // (the difference first: scores far from zero keep their order, and equal ones their weights)
           float2 x = __ffma2_rn(__fadd2_rn(make_float2(__uint_as_float(s[c0 + c]), __uint_as_float(s[c0 + c + 1])), b2), k2, lift2);
-          x.x = pex2(x.x);
-          x.y = pex2(x.y);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
           part[(c >> 1) & 1] = __fadd2_rn(part[(c >> 1) & 1], x);
           w[c / 2] = pack_h(x.x, x.y);
         }
