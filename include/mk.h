@@ -359,8 +359,8 @@ mk_status mk_matvec_engine_status(void* stream);
  * within 0 .. n_rows, a span above max_new, a length below 0 or above max_len, and for rows
  * that are written or read back a span above its length) or a page id outside the pool is
  * recorded in the cache's status word; the sequence or page it concerns is neither written
- * nor read.  (Where cu does not ascend, append and read may leave out further sequences,
- * each as a whole.)  Sequences may share pages that are only read; calls that overlap on the
+ * nor read.  (Where cu does not ascend, further sequences may be left out, each as a whole.)
+ * Sequences may share pages that are only read; calls that overlap on the
  * GPU, and the sequences of one call, must not write the same positions, nor may a call read
  * what another writes meanwhile.  A call that finds a CUDA error pending from an earlier one
  * refuses (MK_ERR_CUDA) and leaves it in place. */

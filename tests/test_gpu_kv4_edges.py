@@ -638,3 +638,50 @@ def test_broadcast_queries(new):
         out = torch.empty((s.rows, 32, 128), dtype=torch.bfloat16, device="cuda")
         s.cache.attend(0, q, out, s.batch)
         check_attention(s, kv, q, out, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("new", [1, 300])
+@pytest.mark.parametrize("power", [-60, -100, -115, -122])
+def test_tiny_queries_under_a_large_scale(power, new, dtype):
+    """Queries of 2^power and a scale that takes that back: the same as queries of ordinary size."""
+    s = Setup(64, 16, [700], [new])
+    kv = s.fill()
+    q = s.rand(new, 32, dtype)
+    small = q * 2.0**power  # (the smallest of 2^-122 are subnormal)
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, small, out, s.batch, scale=2.0**(-power - 3))
+    check_attention(s, kv, small.double() * 2.0**-power, out, dtype, 0.125)
+
+
+@pytest.mark.parametrize("at", [1, 2, 5])
+def test_a_cu_that_does_not_ascend_in_a_batch_packed_by_its_rows(at):
+    """One prompt and single tokens, whose row tiles are found by a search: reported, and every sequence is
+    right or as it was."""
+    from persistent_megakernel_02_b200 import MkError
+
+    new = [600] + [1] * 7
+    lens = [700, 650, 300, 20, 500, 660, 70, 100]
+    s = Setup(64, 8, lens, new)
+    kv = s.fill()
+    cu = s.cu_np.copy()
+    cu[at] -= 20  # in front of the end of the sequence before, or (1) rows of the prompt's for the next one
+    s.batch = s.cache.batch(ints(cu), s.kv_lens, s.rows, 600, 700)
+    q = s.rand(s.rows, 32, "bf16")
+    out = torch.full_like(q, -7.0)
+    s.cache.attend(0, q, out, s.batch)
+    if (np.diff(cu) < 0).any():
+        with pytest.raises(MkError, match="batch numbers"):
+            s.cache.check()
+    s.cache.check()
+    for i in range(8):
+        a, b = cu[i], cu[i + 1]
+        if a >= b or b - a > lens[i]:
+            continue
+        t = Setup.__new__(Setup)
+        t.__dict__.update(s.__dict__)
+        t.cu_np, t.new = cu, [max(0, int(cu[j + 1] - cu[j])) for j in range(8)]
+        want = torch.from_numpy(reference(t, kv, q, i, R.default_scale(64))[0]).cuda()
+        whole = norm_error(out[a:b].double(), want) < NORM["bf16"] + 2.4e-4
+        others = [j for j in range(8) if j != i and cu[j] < b and cu[j + 1] > a]  # share rows with it
+        assert whole or (out[a:b] == -7.0).all() or others, i
