@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreadsA, NT == 1 ? 4 : 2) attn_few(const Att
     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
     // power of two that brings the largest to 2^12 .. 2^13 (rows of zeros and rows
     // with an infinity keep theirs)
-    const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
+    const int e = mx > 0.f && mx < INFINITY ? min(126, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
     const float up = __uint_as_float((uint32_t)(127 + max(e, -126)) << 23);
     const float signed_up = a.scale_log2 < 0.f ? -up : up;
     kscale[t] = kv4_score_scale(fabsf(a.scale_log2) / up * kCode);

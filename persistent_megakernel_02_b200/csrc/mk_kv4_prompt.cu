@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPThreads, 1) attn_prompt(const Kv4AttnSplit a
       // power of two that brings the row's largest to 2^12 .. 2^13 (rows of zeros and rows
       // with an infinity keep theirs); the sign of the scale goes to the queries, so that
       // the maximum of the accumulated scores is the maximum of the scores
-      const int e = mx > 0.f && mx < INFINITY ? min(100, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
+      const int e = mx > 0.f && mx < INFINITY ? min(126, 12 + 127 - (int)(__float_as_uint(mx) >> 23)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + e) << 23), sup = a.scale_log2 < 0.f ? -up : up;
       [[maybe_unused]] uint32_t qt[16];
       kscale = kv4_score_scale(fabsf(a.scale_log2) / up);
